@@ -27,6 +27,8 @@ APPROX_MAX_GROUP = 4
 
 CONV_PASSES = {"fwd": 0, "dgrad": 1, "wgrad": 2}
 
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
 MODEL_EXACT = 0
 MODEL_MITCHELL = 1
 
@@ -37,6 +39,8 @@ EXPORTS = (
     "approx_gemm", "approx_gemm_noalloc", "approx_gemm_noalloc_max_bytes", "approx_gemm_grouped",
     "approx_gemm_strided_batched", "approx_gemm_batched",
     "approx_conv2d_fwd", "approx_conv2d_dgrad", "approx_conv2d_wgrad",
+    "approx_attention_fwd", "approx_attention_bwd", "approx_attention_paged",
+    "approx_dense_fwd", "approx_dense_bwd",
     "approx_gemm_chunks", "approx_conv2d_chunks",
     "approx_profile_enable", "approx_profile_read",
     "approx_status_string", "approx_build_id", "approx_release",
@@ -65,6 +69,12 @@ for _n in ("approx_conv2d_fwd", "approx_conv2d_dgrad", "approx_conv2d_wgrad"):
     getattr(_lib, _n).argtypes = [_i] * 11 + [_vp, _vp, _vp, _vp]
 _lib.approx_gemm_chunks.argtypes = [_i] * 6 + [_ll, _vp, _vp, _vp, _vp]
 _lib.approx_conv2d_chunks.argtypes = [_i] * 12 + [_ll, _vp, _vp]
+_d = ctypes.c_double
+_lib.approx_attention_fwd.argtypes = [_i] * 6 + [_vp, _vp, _i, _d] + [_vp, _i] * 4 + [_vp, _vp]
+_lib.approx_attention_bwd.argtypes = [_i] * 6 + [_vp, _vp, _i, _d] + [_vp, _i] * 5 + [_vp] + [_vp, _i] * 3 + [_vp]
+_lib.approx_attention_paged.argtypes = [_i] * 5 + [_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _d] + [_vp, _i] * 2 + [_vp, _vp]
+_lib.approx_dense_fwd.argtypes = [_i] * 3 + [_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp]
+_lib.approx_dense_bwd.argtypes = [_i] * 3 + [_vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp]
 _lib.approx_status_string.argtypes = [_i]
 _lib.approx_status_string.restype = ctypes.c_char_p
 _lib.approx_build_id.argtypes = []
@@ -306,6 +316,179 @@ def gemm(A, B, transA=False, transB=False, out=None, stream=None):
         out = torch.empty((m, n), dtype=torch.float32, device=A.device)
     approx_gemm(transA, transB, m, n, k, A, A.stride(0), B, B.stride(0), out, out.stride(0), stream)
     return out
+
+
+def _heads(t, what):
+    """Leading dimension of a [tokens, heads, dim] tensor whose heads lie dim apart."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what}: expected [tokens, heads, dim] with contiguous heads, got {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+    least = t.shape[1] * t.shape[2]
+    if t.shape[0] <= 1:
+        return least
+    if t.stride(0) < least:
+        raise ValueError(f"{what}: tokens overlap (stride {t.stride(0)} below {least})")
+    return t.stride(0)
+
+
+def _int32(t, what, device, dims=1):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what}: expected a contiguous {dims}-D int32 tensor on {device}")
+    return t.data_ptr()
+
+
+def _same_device(*tensors):
+    """The tensors' device: one device, the current one (the library queues on it)."""
+    import torch
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: make it the current device")
+    return device
+
+
+def _packed_shapes(q, k, v, cu_q, cu_k):
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError(f"shapes of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not belong together")
+    if cu_q.shape != cu_k.shape or cu_q.numel() < 1:
+        raise ValueError("cu_q and cu_k hold one offset more than there are sequences")
+    return cu_q.numel() - 1
+
+
+def attention_fwd(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=None, stream=None):
+    """Attention of packed prompts with approximate products: q [tokens, heads, dim],
+    k and v [tokens, kv_heads, dim] (views of one projection's output will do),
+    cu_q and cu_k int32 offsets on the GPU. scale defaults to dim ** -0.5.
+    Returns (o, lse); rows of no sequence keep what out and lse hold."""
+    import torch
+    device = _same_device(q, k, v, out, lse)
+    ldq, ldk, ldv = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    nseq = _packed_shapes(q, k, v, cu_q, cu_k)
+    T, H, D = q.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float32, device=device)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=device)
+    if out.shape != q.shape or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("out has q's shape, lse is contiguous [tokens, heads]")
+    _check(_lib.approx_attention_fwd(nseq, H, k.shape[1], D, T, k.shape[0], _int32(cu_q, "cu_q", device),
+                                     _int32(cu_k, "cu_k", device), int(bool(causal)),
+                                     D ** -0.5 if scale is None else float(scale), _ptr(q), ldq, _ptr(k), ldk,
+                                     _ptr(v), ldv, _ptr(out), _heads(out, "out"), _ptr(lse), _stream(stream)),
+           "approx_attention_fwd")
+    return out, lse
+
+
+def attention_bwd(dout, q, k, v, o, lse, cu_q, cu_k, causal=True, scale=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of attention_fwd's o, from its inputs and what it
+    returned; rows of no sequence keep what dq, dk and dv hold."""
+    import torch
+    device = _same_device(q, k, v, o, dout, lse, dq, dk, dv)
+    nseq = _packed_shapes(q, k, v, cu_q, cu_k)
+    T, H, D = q.shape
+    if o.shape != q.shape or dout.shape != q.shape or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("o and dout have q's shape, lse is contiguous [tokens, heads]")
+    dq, dk, dv = (torch.empty(x.shape, dtype=torch.float32, device=device) if g is None else g
+                  for g, x in ((dq, q), (dk, k), (dv, v)))
+    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
+        raise ValueError("dq, dk and dv have the shapes of q, k and v")
+    pairs = []
+    for t, what in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dout, "dout")):
+        pairs += [_ptr(t), _heads(t, what)]
+    grads = []
+    for t, what in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        grads += [_ptr(t), _heads(t, what)]
+    _check(_lib.approx_attention_bwd(nseq, H, k.shape[1], D, T, k.shape[0], _int32(cu_q, "cu_q", device),
+                                     _int32(cu_k, "cu_k", device), int(bool(causal)),
+                                     D ** -0.5 if scale is None else float(scale), *pairs, _ptr(lse), *grads,
+                                     _stream(stream)), "approx_attention_bwd")
+    return dq, dk, dv
+
+
+def attention_paged(q, k_pages, v_pages, block_table, cu_q, k_len, causal=True, scale=None, out=None, lse=None, stream=None):
+    """Attention of new tokens q [tokens, heads, dim] over a paged cache:
+    k_pages and v_pages [pages, page, kv_heads, dim], block_table [sequences,
+    pages per sequence] int32, cu_q offsets of the sequences' new tokens, k_len
+    their cached keys (the new ones included). Returns o; lse ([tokens, heads])
+    is written when given."""
+    import torch
+    device = _same_device(q, k_pages, v_pages, out, lse)
+    T, H, D = q.shape
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != D:
+        raise ValueError("k_pages and v_pages are [pages, page, kv_heads, dim] with q's dim")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages are contiguous")
+    if cu_q.numel() < 1 or k_len.numel() != cu_q.numel() - 1 or block_table.shape[0] != k_len.numel():
+        raise ValueError("cu_q holds one offset more than k_len and block_table hold sequences")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float32, device=device)
+    if out.shape != q.shape or (lse is not None and (lse.shape != (T, H) or not lse.is_contiguous())):
+        raise ValueError("out has q's shape, lse is contiguous [tokens, heads]")
+    _check(_lib.approx_attention_paged(k_len.numel(), H, k_pages.shape[2], D, T, _int32(cu_q, "cu_q", device),
+                                       k_pages.shape[0], k_pages.shape[1], _ptr(k_pages), _ptr(v_pages),
+                                       _int32(block_table, "block_table", device, 2), block_table.shape[1],
+                                       _int32(k_len, "k_len", device), int(bool(causal)),
+                                       D ** -0.5 if scale is None else float(scale), _ptr(q), _heads(q, "q"), _ptr(out),
+                                       _heads(out, "out"), _ptr(lse), _stream(stream)), "approx_attention_paged")
+    return out
+
+
+def _rows(t, what, shape):
+    """Leading dimension of a row-major 2-D tensor of the given shape."""
+    if tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected {tuple(shape)} with contiguous rows, got {tuple(t.shape)} strides {t.stride()}")
+    least = max(1, t.shape[1])
+    if t.shape[0] <= 1:
+        return least
+    if t.stride(0) < least:
+        raise ValueError(f"{what}: rows overlap (stride {t.stride(0)} below {least})")
+    return t.stride(0)
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act {act!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def dense_fwd(x, w, bias=None, act="none", residual=None, keep_z=False, out=None, stream=None):
+    """act(x @ w + bias) + residual with approximate products, x [m, k] and
+    w [k, n]; with keep_z also x @ w + bias, which dense_bwd needs when there
+    is an activation: (y, z)."""
+    import torch
+    device = _same_device(x, w, bias, residual, out)
+    (m, k), n = x.shape, w.shape[1]
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.float32, device=device)
+    z = torch.empty((m, n), dtype=torch.float32, device=device) if keep_z else None
+    if bias is not None and (bias.shape != (n,) or not bias.is_contiguous()):
+        raise ValueError("bias: n contiguous values")
+    _check(_lib.approx_dense_fwd(m, n, k, _ptr(x), _rows(x, "x", (m, k)), _ptr(w), _rows(w, "w", (k, n)), _ptr(bias),
+                                 _activation(act), _ptr(residual),
+                                 max(1, n) if residual is None else _rows(residual, "residual", (m, n)), _ptr(out),
+                                 _rows(out, "out", (m, n)), _ptr(z), max(1, n), _stream(stream)), "approx_dense_fwd")
+    return (out, z) if keep_z else out
+
+
+def dense_bwd(dy, x, w, z=None, act="none", bias=False, dx=None, dw=None, stream=None):
+    """Gradients (dx, dw, db) of dense_fwd's y for dy, with z as keep_z returned
+    it; db is None without a bias. The residual's gradient is dy."""
+    import torch
+    device = _same_device(dy, x, w, z, dx, dw)
+    (m, k), n = x.shape, w.shape[1]
+    if z is None and act != "none":
+        raise ValueError(f"the gradient of {act} needs z")
+    dx = torch.empty((m, k), dtype=torch.float32, device=device) if dx is None else dx
+    dw = torch.empty((k, n), dtype=torch.float32, device=device) if dw is None else dw
+    db = torch.empty((n,), dtype=torch.float32, device=device) if bias else None
+    _check(_lib.approx_dense_bwd(m, n, k, _ptr(x), _rows(x, "x", (m, k)), _ptr(w), _rows(w, "w", (k, n)), _ptr(z),
+                                 max(1, n) if z is None else _rows(z, "z", (m, n)), _activation(act), _ptr(dy),
+                                 _rows(dy, "dy", (m, n)), _ptr(dx), _rows(dx, "dx", (m, k)), _ptr(dw),
+                                 _rows(dw, "dw", (k, n)), _ptr(db), _stream(stream)), "approx_dense_bwd")
+    return dx, dw, db
 
 
 def conv_out_hw(H, W, R, S, stride, pad):

@@ -12,6 +12,8 @@
 #include <vector>
 
 #include "../../include/approx_mul.h"
+#include "attention.h"
+#include "host.h"
 #include "internal.h"
 
 namespace {
@@ -52,6 +54,8 @@ inline bool row_vector_fits(int m, int n, int k)
 struct DeviceTable {
     uint16_t* image = nullptr;  // lane-first LDS image (the allocation; `flat` lies in it)
     uint16_t* flat = nullptr;   // the table in index order (ia << M) | ib, for the row-vector kernel
+    uint16_t* lane_first = nullptr;      // the attention kernels' images (attention.h): lane operand first,
+    uint16_t* uniform_first = nullptr;   // and uniform operand first
     int M = 0;
     bool native = false;        // the native FP32 multiplier is selected (no image)
 };
@@ -74,6 +78,9 @@ int g_exp_bits[kMaxDevices];       // exponent width of the multiplier's format 
 bool g_profile = false;
 std::vector<std::pair<hipEvent_t, hipEvent_t>> g_events;   // GEMM-kernel launches while profiling
 std::map<std::pair<int, hipStream_t>, Arena> g_arenas;
+// A second scratch block per stream, for what a dense layer's backward pass
+// keeps across its GEMM calls (which use the stream's arena).
+std::map<std::pair<int, hipStream_t>, Arena> g_kept;
 // Device memory that a table load or an arena's growth superseded: kept until
 // approx_release, so that work already queued and HIP graphs captured
 // earlier never read freed memory.
@@ -1220,7 +1227,18 @@ extern "C" int approx_lut_load(const uint16_t* lut, int M)
     const size_t img_entries = (size_t)amx::lut_image_bytes(M) / 2;
     const size_t flat_at = (img_entries + 127) & ~(size_t)127;   // entries
     const size_t entries = (size_t)1 << (2 * M);
-    std::vector<uint16_t> img(flat_at + entries + 8, 0);   // + a zero entry (and padding) after the table
+    // then the attention kernels' two images: columns of 2^M entries and two
+    // zeros, by the second operand's mantissa and by the first's
+    const size_t attn_entries = (size_t)amx::attn_image_bytes(M) / 2;
+    const size_t lane_at = (flat_at + entries + 8 + 127) & ~(size_t)127;   // + a zero entry (and padding) after the table
+    const size_t uni_at = (lane_at + attn_entries + 127) & ~(size_t)127;
+    std::vector<uint16_t> img(uni_at + attn_entries, 0);
+    for (int c = 0; c < side; ++c)
+        for (int r = 0; r < side; ++r) {
+            const size_t at = (size_t)c * (side + 2) + r;
+            img[lane_at + at] = lut[((size_t)r << M) | c];
+            img[uni_at + at] = lut[((size_t)c << M) | r];
+        }
     for (int ib = 0; ib < side; ++ib)
         for (int ia = 0; ia < side; ++ia) {
             const uint16_t e = lut[((size_t)ia << M) | ib];
@@ -1245,6 +1263,8 @@ extern "C" int approx_lut_load(const uint16_t* lut, int M)
     if (g_tables[dev].image != nullptr) g_retired.emplace_back(dev, g_tables[dev].image);
     g_tables[dev].image = d;
     g_tables[dev].flat = d + flat_at;
+    g_tables[dev].lane_first = d + lane_at;
+    g_tables[dev].uniform_first = d + uni_at;
     g_tables[dev].M = M;
     g_tables[dev].native = false;
     return APPROX_OK;
@@ -1264,6 +1284,42 @@ extern "C" int approx_native_load(void)
     g_tables[dev].native = true;
     return APPROX_OK;
 }
+
+// What layers.cpp takes of this file's state.
+int amx::host_table(amx::HostTable* t)
+{
+    int rc = current_device(&t->dev);
+    if (rc != APPROX_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        const DeviceTable& d = g_tables[t->dev];
+        if (!d.native && d.image == nullptr) return APPROX_ENOLUT;
+        t->M = d.native ? 0 : d.M;
+        t->lane_first = d.lane_first;
+        t->uniform_first = d.uniform_first;
+    }
+    format_range(t->dev, &t->elo, &t->ehi);
+    t->force_checked = force_checked() ? 1 : 0;
+    return APPROX_OK;
+}
+
+int amx::host_kept(int dev, hipStream_t stream, size_t bytes, char** out)
+{
+    std::lock_guard<std::mutex> lock(g_mu);
+    Arena& a = g_kept[{dev, stream}];
+    if (a.bytes < bytes) {
+        const size_t want = std::max(bytes + bytes / 8, 2 * a.bytes);
+        void* p = nullptr;
+        if (alloc_refused(want) || hipMalloc(&p, want) != hipSuccess) return APPROX_EHIP;
+        if (a.ptr != nullptr) g_retired.emplace_back(dev, a.ptr);
+        a.ptr = p;
+        a.bytes = want;
+    }
+    *out = static_cast<char*>(a.ptr);
+    return APPROX_OK;
+}
+
+int amx::host_scratch(int dev, hipStream_t stream, size_t bytes, char** out) { return arena_get(dev, stream, bytes, out); }
 
 extern "C" int approx_exponent_bits_set(int E)
 {
@@ -1514,12 +1570,14 @@ extern "C" int approx_release(void)
     int rc = APPROX_OK;
     int saved = -1;
     (void)hipGetDevice(&saved);
-    for (auto& kv : g_arenas) {
-        if (kv.second.ptr == nullptr) continue;
-        if (hipSetDevice(kv.first.first) != hipSuccess || hipDeviceSynchronize() != hipSuccess) rc = APPROX_EHIP;
-        if (hipFree(kv.second.ptr) != hipSuccess) rc = APPROX_EHIP;
+    for (auto* arenas : {&g_arenas, &g_kept}) {
+        for (auto& kv : *arenas) {
+            if (kv.second.ptr == nullptr) continue;
+            if (hipSetDevice(kv.first.first) != hipSuccess || hipDeviceSynchronize() != hipSuccess) rc = APPROX_EHIP;
+            if (hipFree(kv.second.ptr) != hipSuccess) rc = APPROX_EHIP;
+        }
+        arenas->clear();
     }
-    g_arenas.clear();
     for (auto& r : g_retired) {
         if (hipSetDevice(r.first) != hipSuccess || hipDeviceSynchronize() != hipSuccess) rc = APPROX_EHIP;
         if (hipFree(r.second) != hipSuccess) rc = APPROX_EHIP;

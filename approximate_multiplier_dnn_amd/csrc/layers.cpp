@@ -1,0 +1,480 @@
+// layers.cpp -- the C ABI's attention and dense-layer calls: argument checks,
+// panel layouts in the stream's scratch arena, and launch plans. Every
+// arithmetic step runs in attention.hip and kernels.hip.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/approx_mul.h"
+#include "attention.h"
+#include "dense.h"
+#include "host.h"
+
+namespace {
+
+using amx::AttnDecodeParams;
+using amx::AttnParams;
+using amx::AttnTensor;
+using amx::HostTable;
+using amx::Word;
+
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// Hands out 256-byte aligned parts of one scratch request: run once without
+// memory to get its size, then with it.
+struct Carver {
+    char* base = nullptr;
+    size_t used = 0;
+    template <typename T>
+    T* take(int64_t count)
+    {
+        T* p = base == nullptr ? nullptr : reinterpret_cast<T*>(base + used);
+        used += (size_t)round_up((int64_t)sizeof(T) * count, 256);
+        return p;
+    }
+};
+
+// Argument checks shared by the attention calls. ld*: floats between tokens.
+int check_heads(int nseq, int heads, int kv_heads, int dim, int total_q, double scale)
+{
+    if (nseq < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || dim < 1 || total_q < 0) return APPROX_EINVAL;
+    if (!std::isfinite(scale) || !(scale > 0.0)) return APPROX_EINVAL;
+    if (dim > amx::kAttnMaxDim) return APPROX_EUNSUPPORTED;
+    if ((int64_t)total_q * heads >= kMaxRows) return APPROX_EUNSUPPORTED;
+    return APPROX_OK;
+}
+
+bool too_small(int ld, int heads, int dim) { return ld < (int64_t)heads * dim; }
+
+// Largest sum of the biased exponents of q and k for which |c s| stays below
+// 2^40: |s| < 2^(sum - 254 + 2) * 128.
+int score_limit(double c) { return 254 + 40 - 9 - (int)std::ceil(std::log2(c)); }
+
+// Chunks of each tile's range, so that the items fill the GPU (about 12
+// resident waves on each of 256 CUs) and a chunk keeps at least 8 blocks of
+// the average range. A function of the shapes only.
+int split_for(int64_t tiles, int64_t blocks)
+{
+    constexpr int64_t kWaves = 256 * 12;
+    const int64_t want = cdiv(kWaves, std::max<int64_t>(1, tiles));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, blocks / 8, amx::kAttnMaxSplits}));
+}
+
+struct Shape {
+    int nseq, H, K, D, total_q, total_k, causal;
+    double scale;
+    const int *cu_q, *cu_k;
+};
+
+void fill_common(AttnParams& p, const Shape& s, const HostTable& t)
+{
+    p.cu_q = s.cu_q;
+    p.cu_k = s.cu_k;
+    p.nseq = s.nseq;
+    p.K = s.K;
+    p.G = s.H / s.K;
+    p.D = s.D;
+    p.D4 = (int)round_up(s.D, 4);
+    p.Dp = s.D <= 64 ? 64 : 128;
+    p.total_q = s.total_q;
+    p.total_k = s.total_k;
+    p.RQ = s.total_q * p.G;
+    p.RQp = (int)round_up(p.RQ, amx::kAttnTile);
+    p.TKp = (int)round_up(std::max(s.total_k, 1), amx::kAttnTile);
+    p.causal = s.causal;
+    p.c = s.scale * kLog2e;
+    p.scale = (float)s.scale;
+    p.M = t.M;
+    p.elo = t.elo;
+    p.ehi = t.ehi;
+    p.smax = score_limit(p.c);
+    p.force_checked = t.force_checked;
+}
+
+enum PanelKind { LANE, TR, ROW };
+
+Word* panel(Carver& c, const AttnParams& p, int Rp, PanelKind kind)
+{
+    return c.take<Word>((int64_t)p.K * Rp * (kind == ROW ? p.Dp : p.D4));
+}
+
+AttnTensor tensor(const float* src, int ld, int R, int G, int Rp)
+{
+    AttnTensor t{};
+    t.src = src;
+    t.ld = ld;
+    t.R = R;
+    t.G = G;
+    t.Rp = Rp;
+    return t;
+}
+
+void fill_decode(AttnDecodeParams& d, const AttnParams& p)
+{
+    d.K = p.K;
+    d.D = p.D;
+    d.D4 = p.D4;
+    d.Dp = p.Dp;
+    d.M = p.M;
+    d.elo = p.elo;
+    d.ehi = p.ehi;
+}
+
+}  // namespace
+
+extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
+                                    const int* cu_q, const int* cu_k, int causal, double scale, const float* q, int ldq,
+                                    const float* k, int ldk, const float* v, int ldv, float* o, int ldo, float* lse,
+                                    void* stream_v)
+{
+    int rc = check_heads(nseq, heads, kv_heads, dim, total_q, scale);
+    if (rc != APPROX_OK) return rc;
+    if (total_k < 0 || (causal != 0 && causal != 1)) return APPROX_EINVAL;
+    if (too_small(ldq, heads, dim) || too_small(ldk, kv_heads, dim) || too_small(ldv, kv_heads, dim) ||
+        too_small(ldo, heads, dim))
+        return APPROX_EINVAL;
+    if (total_k >= kMaxRows) return APPROX_EUNSUPPORTED;
+    if (nseq == 0 || total_q == 0) return APPROX_OK;
+    if (cu_q == nullptr || cu_k == nullptr || q == nullptr || o == nullptr) return APPROX_EINVAL;
+    if (total_k > 0 && (k == nullptr || v == nullptr)) return APPROX_EINVAL;
+    HostTable t;
+    rc = amx::host_table(&t);
+    if (rc != APPROX_OK) return rc;
+    hipStream_t stream = static_cast<hipStream_t>(stream_v);
+
+    AttnParams p{};
+    fill_common(p, Shape{nseq, heads, kv_heads, dim, total_q, total_k, causal, scale, cu_q, cu_k}, t);
+    p.lut = t.lane_first;
+    p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + nseq);
+    p.splits = split_for((int64_t)cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq));
+    p.items = (int64_t)p.tiles * p.K * p.splits;
+    if (p.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    p.o = o;
+    p.ldo = ldo;
+    p.lse = lse;
+
+    AttnDecodeParams d{};
+    fill_decode(d, p);
+    d.count = 3;
+    d.t[0] = tensor(q, ldq, p.RQ, p.G, p.RQp);
+    d.t[1] = tensor(k, ldk, total_k, 1, p.TKp);
+    d.t[2] = tensor(v, ldv, total_k, 1, p.TKp);
+    Carver c;
+    for (int pass = 0; pass < 2; ++pass) {
+        c.used = 0;
+        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        d.t[0].lane = panel(c, p, p.RQp, LANE);
+        d.t[1].tr = panel(c, p, p.TKp, TR);
+        d.t[2].row = panel(c, p, p.TKp, ROW);
+        if (p.splits > 1) {
+            const int64_t rows = (int64_t)p.splits * p.K * p.RQ;
+            p.part0 = c.take<float>(rows * p.Dp);
+            p.part_m = c.take<double>(rows);
+            p.part_l = c.take<double>(rows);
+        }
+        if (pass == 0) {
+            rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
+            if (rc != APPROX_OK) return rc;
+        }
+    }
+    p.stats = d.stats;
+    p.q_lane = d.t[0].lane;
+    p.k_tr = d.t[1].tr;
+    p.v_row = d.t[2].row;
+    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
+    return amx::launch_attn_fwd(p, stream) == hipSuccess ? APPROX_OK : APPROX_EHIP;
+}
+
+extern "C" int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
+                                    const int* cu_q, const int* cu_k, int causal, double scale, const float* q, int ldq,
+                                    const float* k, int ldk, const float* v, int ldv, const float* o, int ldo,
+                                    const float* dout, int lddo, const float* lse, float* dq, int lddq, float* dk,
+                                    int lddk, float* dv, int lddv, void* stream_v)
+{
+    int rc = check_heads(nseq, heads, kv_heads, dim, total_q, scale);
+    if (rc != APPROX_OK) return rc;
+    if (total_k < 0 || (causal != 0 && causal != 1)) return APPROX_EINVAL;
+    if (too_small(ldq, heads, dim) || too_small(ldk, kv_heads, dim) || too_small(ldv, kv_heads, dim) ||
+        too_small(ldo, heads, dim) || too_small(lddo, heads, dim) || too_small(lddq, heads, dim) ||
+        too_small(lddk, kv_heads, dim) || too_small(lddv, kv_heads, dim))
+        return APPROX_EINVAL;
+    if (total_k >= kMaxRows) return APPROX_EUNSUPPORTED;
+    if (nseq == 0 || (total_q == 0 && total_k == 0)) return APPROX_OK;
+    if (cu_q == nullptr || cu_k == nullptr) return APPROX_EINVAL;
+    if (total_q > 0 && (q == nullptr || o == nullptr || dout == nullptr || lse == nullptr || dq == nullptr)) return APPROX_EINVAL;
+    if (total_k > 0 && (k == nullptr || v == nullptr || dk == nullptr || dv == nullptr)) return APPROX_EINVAL;
+    HostTable t;
+    rc = amx::host_table(&t);
+    if (rc != APPROX_OK) return rc;
+    hipStream_t stream = static_cast<hipStream_t>(stream_v);
+
+    AttnParams p{};
+    fill_common(p, Shape{nseq, heads, kv_heads, dim, total_q, total_k, causal, scale, cu_q, cu_k}, t);
+    p.RQp = std::max(p.RQp, amx::kAttnTile);
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.lddq = lddq;
+    p.lddk = lddk;
+    p.lddv = lddv;
+    AttnParams kp = p;               // the keys' pass
+    p.lut = t.lane_first;
+    kp.lut = t.uniform_first;
+    p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + nseq);
+    kp.tiles = (int)(cdiv(total_k, amx::kAttnTile) + nseq);
+    p.splits = split_for(cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq));
+    kp.splits = split_for(cdiv(total_k, amx::kAttnTile) * p.K, cdiv(p.RQ, (int64_t)amx::kAttnBlock * nseq));
+    p.items = (int64_t)p.tiles * p.K * p.splits;
+    kp.items = (int64_t)kp.tiles * p.K * kp.splits;
+    if (p.items >= INT32_MAX || kp.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+
+    AttnDecodeParams d{};
+    fill_decode(d, p);
+    d.count = 4;
+    d.t[0] = tensor(q, ldq, p.RQ, p.G, p.RQp);
+    d.t[1] = tensor(dout, lddo, p.RQ, p.G, p.RQp);
+    d.t[2] = tensor(k, ldk, total_k, 1, p.TKp);
+    d.t[3] = tensor(v, ldv, total_k, 1, p.TKp);
+    d.o = o;
+    d.ldo = ldo;
+    d.lse = lse;
+    Carver c;
+    for (int pass = 0; pass < 2; ++pass) {
+        c.used = 0;
+        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        for (int i = 0; i < 4; ++i) {
+            d.t[i].lane = panel(c, p, d.t[i].Rp, LANE);
+            d.t[i].tr = panel(c, p, d.t[i].Rp, TR);
+            d.t[i].row = i == 3 ? nullptr : panel(c, p, d.t[i].Rp, ROW);
+        }
+        d.delta = c.take<float>((int64_t)p.K * p.RQp);
+        d.rowlse = c.take<float>((int64_t)p.K * p.RQp);
+        // both passes' partials share one place: dQ is summed before the keys' pass starts
+        const size_t before = c.used;
+        if (p.splits > 1) p.part0 = c.take<float>((int64_t)p.splits * p.K * p.RQ * p.Dp);
+        const size_t after = c.used;
+        c.used = before;
+        if (kp.splits > 1) {
+            kp.part0 = c.take<float>((int64_t)kp.splits * p.K * total_k * p.Dp);
+            kp.part1 = c.take<float>((int64_t)kp.splits * p.K * total_k * p.Dp);
+        }
+        c.used = std::max(c.used, after);
+        if (pass == 0) {
+            rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
+            if (rc != APPROX_OK) return rc;
+        }
+    }
+    for (AttnParams* a : {&p, &kp}) {
+        a->stats = d.stats;
+        a->q_lane = d.t[0].lane; a->q_tr = d.t[0].tr; a->q_row = d.t[0].row;
+        a->do_lane = d.t[1].lane; a->do_tr = d.t[1].tr; a->do_row = d.t[1].row;
+        a->k_lane = d.t[2].lane; a->k_tr = d.t[2].tr; a->k_row = d.t[2].row;
+        a->v_lane = d.t[3].lane; a->v_tr = d.t[3].tr;
+        a->delta = d.delta;
+        a->rowlse = d.rowlse;
+    }
+    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
+    if (total_q > 0 && amx::launch_attn_bwd(p, false, stream) != hipSuccess) return APPROX_EHIP;
+    if (total_k > 0 && amx::launch_attn_bwd(kp, true, stream) != hipSuccess) return APPROX_EHIP;
+    return APPROX_OK;
+}
+
+extern "C" int approx_attention_paged(int nseq, int heads, int kv_heads, int dim, int total_q, const int* cu_q,
+                                      int num_pages, int page, const float* k_pages, const float* v_pages,
+                                      const int* block_table, int table_ld, const int* k_len, int causal, double scale,
+                                      const float* q, int ldq, float* o, int ldo, float* lse, void* stream_v)
+{
+    int rc = check_heads(nseq, heads, kv_heads, dim, total_q, scale);
+    if (rc != APPROX_OK) return rc;
+    if (num_pages < 0 || page < 1 || table_ld < 0 || (causal != 0 && causal != 1)) return APPROX_EINVAL;
+    if (too_small(ldq, heads, dim) || too_small(ldo, heads, dim)) return APPROX_EINVAL;
+    if ((int64_t)num_pages * page >= kMaxRows || (int64_t)table_ld * page >= kMaxRows) return APPROX_EUNSUPPORTED;
+    if (nseq == 0 || total_q == 0) return APPROX_OK;
+    if (cu_q == nullptr || k_len == nullptr || q == nullptr || o == nullptr) return APPROX_EINVAL;
+    if (num_pages == 0) table_ld = 0;                 // no page: every row is empty
+    if (table_ld > 0 && (block_table == nullptr || k_pages == nullptr || v_pages == nullptr)) return APPROX_EINVAL;
+    HostTable t;
+    rc = amx::host_table(&t);
+    if (rc != APPROX_OK) return rc;
+    hipStream_t stream = static_cast<hipStream_t>(stream_v);
+
+    amx::PagedParams p{};
+    p.cu_q = cu_q;
+    p.k_len = k_len;
+    p.table = block_table;
+    p.kp = k_pages;
+    p.vp = v_pages;
+    p.nseq = nseq;
+    p.K = kv_heads;
+    p.G = heads / kv_heads;
+    p.D = dim;
+    p.D4 = (int)round_up(dim, 4);
+    p.Dp = dim <= 64 ? 64 : 128;
+    p.total_q = total_q;
+    p.RQ = total_q * p.G;
+    p.page = page;
+    p.num_pages = num_pages;
+    p.table_ld = table_ld;
+    p.fd_page = amx::make_fastdiv((uint32_t)page);
+    p.causal = causal;
+    p.vec = dim % 4 == 0 && (reinterpret_cast<uintptr_t>(k_pages) & 15) == 0 ? 1 : 0;
+    p.c = scale * kLog2e;
+    p.M = t.M;
+    p.elo = t.elo;
+    p.ehi = t.ehi;
+    p.smax = score_limit(p.c);
+    p.force_checked = t.force_checked;
+    p.lut = t.uniform_first;
+    const int64_t rows = cdiv(total_q, nseq) * p.G;         // of an average sequence
+    p.NR = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+    p.blocks = (int)(cdiv(p.RQ, p.NR) + nseq);
+    const int64_t keys = std::max<int64_t>(1, (int64_t)table_ld * page);
+    const int64_t heads_blocks = std::max<int64_t>(1, std::max<int64_t>(cdiv(p.RQ, p.NR), nseq) * p.K);
+    const int64_t want = cdiv(256 * 12 * 2, heads_blocks);
+    p.chunk = (int)std::max<int64_t>(64, round_up(cdiv(keys, want), 64));
+    p.splits = (int)cdiv(keys, p.chunk);
+    p.items = (int64_t)p.blocks * p.K * p.splits;
+    if (p.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    p.o = o;
+    p.ldo = ldo;
+    p.lse = lse;
+
+    AttnDecodeParams d{};
+    d.K = p.K;
+    d.D = p.D;
+    d.D4 = p.D4;
+    d.Dp = p.Dp;
+    d.M = p.M;
+    d.elo = p.elo;
+    d.ehi = p.ehi;
+    d.count = 1;
+    // a block's columns may start at the last row: a tile of zero rows follows
+    const int Rp = (int)round_up(p.RQ, amx::kAttnTile) + amx::kAttnTile;
+    d.t[0] = tensor(q, ldq, p.RQ, p.G, Rp);
+    p.Fp = d.t[0].Fp = Rp;
+    Carver c;
+    for (int pass = 0; pass < 2; ++pass) {
+        c.used = 0;
+        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        d.t[0].flat = c.take<Word>((int64_t)p.K * p.D4 * p.Fp);
+        if (p.splits > 1) {
+            const int64_t n = (int64_t)p.splits * p.K * p.RQ;
+            p.part0 = c.take<float>(n * p.Dp);
+            p.part_m = c.take<double>(n);
+            p.part_l = c.take<double>(n);
+        }
+        if (pass == 0) {
+            rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
+            if (rc != APPROX_OK) return rc;
+        }
+    }
+    p.stats = d.stats;
+    p.q_flat = d.t[0].flat;
+    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
+    return amx::launch_attn_paged(p, stream) == hipSuccess ? APPROX_OK : APPROX_EHIP;
+}
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+extern "C" int approx_dense_fwd(int m, int n, int k, const float* X, int ldx, const float* W, int ldw, const float* bias,
+                                int act, const float* residual, int ldr, float* Y, int ldy, float* Z, int ldz, void* stream_v)
+{
+    if (act < 0 || act >= amx::ACT_COUNT) return APPROX_EINVAL;
+    if (m < 0 || n < 0 || k < 0 || ldy < std::max(1, n)) return APPROX_EINVAL;
+    if (residual != nullptr && ldr < std::max(1, n)) return APPROX_EINVAL;
+    if (Z != nullptr && ldz < std::max(1, n)) return APPROX_EINVAL;
+    if (m > 0 && n > 0 && Y == nullptr) return APPROX_EINVAL;
+    // the sums go to Z when it is wanted, else to Y
+    float* sums = Z != nullptr ? Z : Y;
+    const int lds = Z != nullptr ? ldz : ldy;
+    const int rc = approx_gemm(0, 0, m, n, k, X, ldx, W, ldw, sums, lds, stream_v);
+    if (rc != APPROX_OK || m == 0 || n == 0) return rc;
+    if (bias == nullptr && act == amx::ACT_NONE && residual == nullptr && Z == nullptr) return APPROX_OK;
+    amx::EpilogueParams p{};
+    p.sums = sums;
+    p.bias = bias;
+    p.residual = residual;
+    p.z = Z;
+    p.y = Y;
+    p.lds = lds;
+    p.ldr = ldr;
+    p.ldz = ldz;
+    p.ldy = ldy;
+    p.m = m;
+    p.n = n;
+    p.act = act;
+    p.vec = ((n | lds | ldy | (residual ? ldr : 0)) & 3) == 0 && aligned16(sums) && aligned16(Y) && aligned16(bias) && aligned16(residual);
+    return amx::launch_epilogue(p, static_cast<hipStream_t>(stream_v)) == hipSuccess ? APPROX_OK : APPROX_EHIP;
+}
+
+extern "C" int approx_dense_bwd(int m, int n, int k, const float* X, int ldx, const float* W, int ldw, const float* Z, int ldz,
+                                int act, const float* dY, int lddy, float* dX, int lddx, float* dW, int lddw, float* db,
+                                void* stream_v)
+{
+    if (act < 0 || act >= amx::ACT_COUNT) return APPROX_EINVAL;
+    if (m < 0 || n < 0 || k < 0 || lddy < std::max(1, n)) return APPROX_EINVAL;
+    if (act != amx::ACT_NONE && ldz < std::max(1, n)) return APPROX_EINVAL;
+    if (dX != nullptr && (lddx < std::max(1, k) || ldw < std::max(1, n))) return APPROX_EINVAL;
+    if (dW != nullptr && (lddw < std::max(1, n) || ldx < std::max(1, k))) return APPROX_EINVAL;
+    if (m > 0 && n > 0 && (dY == nullptr || (act != amx::ACT_NONE && Z == nullptr))) return APPROX_EINVAL;
+    if (m > 0 && k > 0 && n > 0 && ((dX != nullptr && W == nullptr) || (dW != nullptr && X == nullptr))) return APPROX_EINVAL;
+    HostTable t;
+    int rc = amx::host_table(&t);
+    if (rc != APPROX_OK) return rc;
+    hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    const float* dz = dY;
+    int lddz = lddy;
+    if (n > 0 && (db != nullptr || (act != amx::ACT_NONE && m > 0))) {
+        amx::DzParams p{};
+        p.dy = dY;
+        p.z = act != amx::ACT_NONE ? Z : nullptr;
+        p.lddy = lddy;
+        p.ldz = ldz;
+        p.m = m;
+        p.n = n;
+        p.act = act;
+        // about 1024 workgroups, at least 16 rows each
+        p.rows = (int)std::max<int64_t>(16, cdiv((int64_t)m * cdiv(n, 64), 1024));
+        const int64_t chunks = cdiv(std::max(m, 1), p.rows);
+        Carver c;
+        float* own = nullptr;
+        for (int pass = 0; pass < 2; ++pass) {
+            c.used = 0;
+            own = act != amx::ACT_NONE ? c.take<float>((int64_t)m * n) : nullptr;
+            p.part = db != nullptr ? c.take<double>(chunks * n) : nullptr;
+            if (pass == 0) {
+                rc = amx::host_kept(t.dev, stream, c.used, &c.base);
+                if (rc != APPROX_OK) return rc;
+            }
+        }
+        p.dz = own;
+        if (amx::launch_dz(p, db, stream) != hipSuccess) return APPROX_EHIP;
+        if (own != nullptr) {
+            dz = own;
+            lddz = n;
+        }
+    }
+    // dX = dz W^T and dW = X^T dz in one grouped call
+    int count = 0, tA[2], tB[2], ms[2], ns[2], ks[2], las[2], lbs[2], lcs[2];
+    const float *As[2], *Bs[2];
+    float* Cs[2];
+    auto add = [&](int ta, int tb, int mm, int nn, int kk, const float* A, int la, const float* B, int lb, float* C, int lc) {
+        if (mm == 0 || nn == 0) return;
+        tA[count] = ta; tB[count] = tb; ms[count] = mm; ns[count] = nn; ks[count] = kk;
+        As[count] = A; las[count] = la; Bs[count] = B; lbs[count] = lb; Cs[count] = C; lcs[count] = lc;
+        ++count;
+    };
+    if (dX != nullptr) add(0, 1, m, k, n, dz, lddz, W, ldw, dX, lddx);
+    if (dW != nullptr) add(1, 0, k, n, m, X, ldx, dz, lddz, dW, lddw);
+    if (count == 0) return APPROX_OK;
+    return approx_gemm_grouped(count, tA, tB, ms, ns, ks, As, las, Bs, lbs, Cs, lcs, stream_v);
+}

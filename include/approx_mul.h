@@ -317,6 +317,109 @@ int approx_conv2d_chunks(int pass, int N, int H, int W, int C, int K, int R, int
                          long long count, const long long *idx, long long *chunk);
 
 /*
+ * Attention with approximate products over packed prompts.
+ *
+ * Sequence b holds the query tokens cu_q[b] .. cu_q[b+1]-1 and the key tokens
+ * cu_k[b] .. cu_k[b+1]-1 (device arrays of nseq + 1 ascending offsets).
+ * Token t, head h of a tensor X is the dim contiguous floats at
+ * X + t * ldX + h * dim; k and v have kv_heads heads, and query head h reads
+ * kv head h / (heads / kv_heads). With T the multiplier's product (the loaded
+ * table or the native multiplier), for query row i and the keys j it sees
+ * (all of its sequence; causal = 1: the query sequence's last token sees every
+ * key, each earlier one a key fewer):
+ *   s_ij = sum over d, FP32, ascending from +0, of T(q_id, k_jd)
+ *   t_ij = scale * log2(e) * s_ij                         (64 bits)
+ *   E_ij = 2^(t_ij - ceil(max_j t_ij)), rounded once to FP32; 0 below 2^-64
+ *   o_id = (sum over j of T(E_ij, v_jd)) / l_i, l_i = sum over j of E_ij
+ *   lse_i = ln(sum over j of 2^t_ij), rounded once to FP32
+ * Keys a row does not see have no part in it, whatever they hold. A row that
+ * sees no key, or whose scores are all -Inf, gets o = 0 and lse = -Inf; a row
+ * with a NaN or +Inf score gets NaN. o's sums run in FP32 in an order that
+ * depends on the shapes only: the same inputs give the same bits.
+ * lse ([total_q][heads]) may be NULL in the forward pass.
+ *
+ * approx_attention_bwd: gradients for dout (o's gradient), from o and lse as
+ * the forward pass left them:
+ *   P_ij = 2^(t_ij - lse_i log2(e)), rounded once; 0 below 2^-64
+ *   D_i = sum over d of dout_id o_id (exact products, 64 bits), rounded once
+ *   dP_ij = sum over d, FP32, ascending from +0, of T(dout_id, v_jd)
+ *   dS_ij = P_ij (dP_ij - D_i) (64 bits), rounded once; 0 below 2^-64
+ *   dq_i = scale sum over j of T(dS_ij, k_j)
+ *   dk_j = scale sum over i of T(q_i, dS_ij);  dv_j = sum over i of T(dout_i, P_ij)
+ * with i over the rows of every head of j's group. dq, dk and dv are
+ * overwritten.
+ *
+ * Rows of the outputs that belong to no sequence keep what they hold.
+ * Offsets are clamped to [0, total] and to the largest offset before them, so
+ * wrong ones give wrong rows but no access outside the tensors. total_q and
+ * total_k are the tokens of the tensors.
+ * Errors: APPROX_EINVAL (sizes, heads not a multiple of kv_heads, a leading
+ * dimension below heads * dim, causal not 0 or 1, scale not finite and
+ * positive, NULL pointers), APPROX_EUNSUPPORTED (dim above 128, 2^30 rows or
+ * more), APPROX_ENOLUT, APPROX_EHIP.
+ */
+int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
+                         const int *cu_q, const int *cu_k, int causal, double scale,
+                         const float *q, int ldq, const float *k, int ldk, const float *v, int ldv,
+                         float *o, int ldo, float *lse, void *stream);
+int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
+                         const int *cu_q, const int *cu_k, int causal, double scale,
+                         const float *q, int ldq, const float *k, int ldk, const float *v, int ldv,
+                         const float *o, int ldo, const float *dout, int lddo, const float *lse,
+                         float *dq, int lddq, float *dk, int lddk, float *dv, int lddv, void *stream);
+
+/*
+ * Attention of new tokens over a paged cache, with the products, scores and
+ * rounding of approx_attention_fwd. Sequence b has the query tokens cu_q[b] ..
+ * cu_q[b+1]-1 (one, or a chunk) and k_len[b] cached keys (device int32), those
+ * of its new tokens among them; its key j lies in page
+ * block_table[b * table_ld + j / page] at place j % page. k_pages and v_pages
+ * are [num_pages][page][kv_heads][dim]. causal = 1: the last new token sees
+ * every key, each earlier one a key fewer. A row without keys gets o = 0 and
+ * lse = -Inf; lse may be NULL. k_len is clamped to table_ld * page, and keys
+ * whose page number lies outside [0, num_pages) are not seen by any row, so
+ * wrong lengths and tables give wrong rows but no access outside the cache.
+ * Errors: as approx_attention_fwd; APPROX_EUNSUPPORTED also for 2^30 places
+ * or more in the cache or in a sequence's table row.
+ */
+int approx_attention_paged(int nseq, int heads, int kv_heads, int dim, int total_q, const int *cu_q,
+                           int num_pages, int page, const float *k_pages, const float *v_pages,
+                           const int *block_table, int table_ld, const int *k_len, int causal, double scale,
+                           const float *q, int ldq, float *o, int ldo, float *lse, void *stream);
+
+/*
+ * Dense layer with bias, activation and residual:
+ *   z = X W + bias,  y = act(z) + residual
+ * X is m x k, W k x n, bias n values (or NULL), residual m x n (or NULL); the
+ * product and its summation order are approx_gemm's. Y gets y and, when not
+ * NULL, Z gets z (what the backward pass of an activation needs). Bias,
+ * activation and residual are FP32; the activations are APPROX_ACT_NONE, RELU,
+ * GELU (z Phi(z), the Gaussian's distribution function) and SILU (z / (1 +
+ * e^-z)).
+ *
+ * approx_dense_bwd: from dY, the gradient of y (the residual's gradient is dY
+ * itself),
+ *   dz = dY act'(z) (64 bits), rounded once to FP32
+ *   dX = dz W^T, dW = X^T dz (approx_gemm's products and order)
+ *   db = column sums of dz (64 bits), rounded once
+ * Any of dX, dW and db may be NULL and is then left out. Z is not read for
+ * APPROX_ACT_NONE. Outputs are overwritten and must not overlap inputs or each
+ * other.
+ * Errors: APPROX_EINVAL (sizes, leading dimensions, unknown activation, NULL
+ * pointers), and approx_gemm's.
+ */
+#define APPROX_ACT_NONE 0
+#define APPROX_ACT_RELU 1
+#define APPROX_ACT_GELU 2
+#define APPROX_ACT_SILU 3
+int approx_dense_fwd(int m, int n, int k, const float *X, int ldx, const float *W, int ldw,
+                     const float *bias, int act, const float *residual, int ldr, float *Y, int ldy,
+                     float *Z, int ldz, void *stream);
+int approx_dense_bwd(int m, int n, int k, const float *X, int ldx, const float *W, int ldw,
+                     const float *Z, int ldz, int act, const float *dY, int lddy,
+                     float *dX, int lddx, float *dW, int lddw, float *db, void *stream);
+
+/*
  * Kernel timing for benchmarks. While enabled (on != 0), every compute call
  * records a HIP event pair around its GEMM kernel, on the call's stream.
  * approx_profile_read waits for the recorded events, returns the number of
