@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libapproxmul.so")
 CSRC = os.path.join(HERE, "csrc")
 HEADER = os.path.join(ROOT, "include", "approx_mul.h")
-SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "attention.hip", "dense.hip", "api.cpp", "layers.cpp", "lut_build.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "attention.hip", "paged.hip", "dense.hip", "api.cpp", "layers.cpp", "lut_build.cpp")]
 
 # Packed FP32 VALU instructions are disabled for every HIP translation unit.
 HIPCC_FLAGS = [

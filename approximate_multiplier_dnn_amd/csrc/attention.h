@@ -29,7 +29,7 @@ constexpr int kAttnMaxSplits = 32;
 // of 8-byte Words:
 //   lane: [K][D4 / 4][Rp][4]  rows across the lanes, reduction over D
 //   tr:   [K][Rp / 16][D4][16]  16 rows as uniform columns, reduction over D
-//   row:  [K][Rp][Dp]         columns d uniform, reduction over the rows
+//   row:  [K][Dp / 16][Rp][16]  16 columns uniform, reduction over the rows
 //   flat: [K][D4][Fp]         as tr, a block of uniform columns from any row on
 // with Rp the rows rounded up to 64, D4 and Dp the dimension rounded up to 4
 // and 16; the padding holds zero operands.
@@ -54,6 +54,7 @@ struct AttnDecodeParams {
     const float* lse;    // [tokens][heads]
     float* delta;
     float* rowlse;
+    int* next;           // two item counters to clear, or null
 };
 
 // Attention of packed sequences. cu_q / cu_k: device offsets (nseq + 1).
@@ -61,6 +62,7 @@ struct AttnParams {
     const int* cu_q;
     const int* cu_k;
     int nseq, K, G, D, D4, Dp;
+    int NW, TT;               // waves of a tile (Dp / 16); tiles of a workgroup (set by the launcher)
     int total_q, total_k, RQ, RQp, TKp;
     int causal;
     double c;                 // scale * log2(e)
@@ -75,7 +77,8 @@ struct AttnParams {
     const float* delta;
     const float* rowlse;
     int tiles, splits;        // row tiles (upper bound) per kv head; chunks of each tile's range
-    int64_t items;
+    int64_t items;            // set by the launcher
+    int* next;                // item counter, cleared by the decode launch
     // outputs (token-major, ld floats between tokens)
     float *o, *lse, *dq, *dk, *dv;
     int64_t ldo, lddq, lddk, lddv;

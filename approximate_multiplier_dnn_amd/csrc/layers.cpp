@@ -55,14 +55,14 @@ bool too_small(int ld, int heads, int dim) { return ld < (int64_t)heads * dim; }
 // 2^40: |s| < 2^(sum - 254 + 2) * 128.
 int score_limit(double c) { return 254 + 40 - 9 - (int)std::ceil(std::log2(c)); }
 
-// Chunks of each tile's range, so that the items fill the GPU (about 12
-// resident waves on each of 256 CUs) and a chunk keeps at least 8 blocks of
-// the average range. A function of the shapes only.
-int split_for(int64_t tiles, int64_t blocks)
+// Chunks of each tile's range, so that the items (tiles x chunks) are about
+// three for each of 768 resident workgroups, and a chunk keeps at least two
+// steps of 16 NW of the average range. A function of the shapes only.
+int split_for(int64_t tiles, int64_t blocks, int NW)
 {
-    constexpr int64_t kWaves = 256 * 12;
-    const int64_t want = cdiv(kWaves, std::max<int64_t>(1, tiles));
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, blocks / 8, amx::kAttnMaxSplits}));
+    constexpr int64_t kItems = 3 * 768;
+    const int64_t want = cdiv(kItems, std::max<int64_t>(1, tiles));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, blocks / (2 * NW), amx::kAttnMaxSplits}));
 }
 
 struct Shape {
@@ -80,7 +80,8 @@ void fill_common(AttnParams& p, const Shape& s, const HostTable& t)
     p.G = s.H / s.K;
     p.D = s.D;
     p.D4 = (int)round_up(s.D, 4);
-    p.Dp = s.D <= 64 ? 64 : 128;
+    p.Dp = (int)round_up(s.D, 16);
+    p.NW = p.Dp / 16;
     p.total_q = s.total_q;
     p.total_k = s.total_k;
     p.RQ = s.total_q * p.G;
@@ -151,9 +152,8 @@ extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, 
     fill_common(p, Shape{nseq, heads, kv_heads, dim, total_q, total_k, causal, scale, cu_q, cu_k}, t);
     p.lut = t.lane_first;
     p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + nseq);
-    p.splits = split_for((int64_t)cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq));
-    p.items = (int64_t)p.tiles * p.K * p.splits;
-    if (p.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    p.splits = split_for((int64_t)cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq), p.NW);
+    if ((int64_t)p.tiles * p.K * p.splits >= INT32_MAX / 2) return APPROX_EUNSUPPORTED;
     p.o = o;
     p.ldo = ldo;
     p.lse = lse;
@@ -168,6 +168,7 @@ extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, 
     for (int pass = 0; pass < 2; ++pass) {
         c.used = 0;
         d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        d.next = c.take<int>(2);
         d.t[0].lane = panel(c, p, p.RQp, LANE);
         d.t[1].tr = panel(c, p, p.TKp, TR);
         d.t[2].row = panel(c, p, p.TKp, ROW);
@@ -183,6 +184,7 @@ extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, 
         }
     }
     p.stats = d.stats;
+    p.next = d.next;
     p.q_lane = d.t[0].lane;
     p.k_tr = d.t[1].tr;
     p.v_row = d.t[2].row;
@@ -227,11 +229,10 @@ extern "C" int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, 
     kp.lut = t.uniform_first;
     p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + nseq);
     kp.tiles = (int)(cdiv(total_k, amx::kAttnTile) + nseq);
-    p.splits = split_for(cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq));
-    kp.splits = split_for(cdiv(total_k, amx::kAttnTile) * p.K, cdiv(p.RQ, (int64_t)amx::kAttnBlock * nseq));
-    p.items = (int64_t)p.tiles * p.K * p.splits;
-    kp.items = (int64_t)kp.tiles * p.K * kp.splits;
-    if (p.items >= INT32_MAX || kp.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    p.splits = split_for(cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq), p.NW);
+    kp.splits = split_for(cdiv(total_k, amx::kAttnTile) * p.K, cdiv(p.RQ, (int64_t)amx::kAttnBlock * nseq), p.NW);
+    if ((int64_t)p.tiles * p.K * p.splits >= INT32_MAX / 2 || (int64_t)kp.tiles * p.K * kp.splits >= INT32_MAX / 2)
+        return APPROX_EUNSUPPORTED;
 
     AttnDecodeParams d{};
     fill_decode(d, p);
@@ -247,6 +248,7 @@ extern "C" int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, 
     for (int pass = 0; pass < 2; ++pass) {
         c.used = 0;
         d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        d.next = c.take<int>(2);
         for (int i = 0; i < 4; ++i) {
             d.t[i].lane = panel(c, p, d.t[i].Rp, LANE);
             d.t[i].tr = panel(c, p, d.t[i].Rp, TR);
@@ -271,6 +273,7 @@ extern "C" int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, 
     }
     for (AttnParams* a : {&p, &kp}) {
         a->stats = d.stats;
+        a->next = a == &p ? d.next : d.next + 1;
         a->q_lane = d.t[0].lane; a->q_tr = d.t[0].tr; a->q_row = d.t[0].row;
         a->do_lane = d.t[1].lane; a->do_tr = d.t[1].tr; a->do_row = d.t[1].row;
         a->k_lane = d.t[2].lane; a->k_tr = d.t[2].tr; a->k_row = d.t[2].row;
