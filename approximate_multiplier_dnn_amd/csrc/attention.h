@@ -30,17 +30,16 @@ constexpr int kAttnMaxSplits = 32;
 //   lane: [K][D4 / 4][Rp][4]  rows across the lanes, reduction over D
 //   tr:   [K][Rp / 16][D4][16]  16 rows as uniform columns, reduction over D
 //   row:  [K][Dp / 16][Rp][16]  16 columns uniform, reduction over the rows
-//   flat: [K][D4][Fp]         as tr, a block of uniform columns from any row on
 // with Rp the rows rounded up to 64, D4 and Dp the dimension rounded up to 4
 // and 16; the padding holds zero operands.
 struct AttnTensor {
     const float* src;
     int64_t ld;          // floats between tokens
-    int R, G, Rp, Fp;
+    int R, G, Rp;
+    FastDiv fd_G;
     Word* lane;
     Word* tr;
     Word* row;
-    Word* flat;
 };
 
 struct AttnDecodeParams {
@@ -108,9 +107,9 @@ struct PagedParams {
     const int* table;         // [nseq][table_ld] page numbers
     const float* kp;          // [num_pages][page][K][D]
     const float* vp;
-    const Word* q_flat;       // [K][D4][Fp]: rows as uniform columns from any row on
-    const uint32_t* stats;    // exponent range of q
-    int nseq, K, G, D, D4, Dp, Fp, total_q, RQ;
+    const float* q;
+    int64_t ldq;
+    int nseq, K, G, D, D4, Dp, total_q, RQ;
     int page, num_pages, table_ld;
     FastDiv fd_page;
     int causal, vec;          // vec: 16-byte loads of the keys
@@ -120,7 +119,6 @@ struct PagedParams {
     const uint16_t* lut;      // uniform operand first
     int NR;                   // rows of a block (4, 8 or 16)
     int blocks, splits, chunk;   // row blocks (upper bound) per kv head; chunks of `chunk` keys
-    int64_t items;
     float *o, *lse;
     int64_t ldo;
     float* part0;

@@ -41,27 +41,28 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
     for (int64_t item = blockIdx.x; item < (int64_t)blocks * p.K; item += gridDim.x) {
         const int h = (int)(item / blocks), r0 = (int)(item - (int64_t)h * blocks) * kAttnTile;
         __syncthreads();
-        if (vec) {
-            const int per = p.Dp / 4;
-            for (int i = tid; i < kAttnTile * per; i += kDecodeThreads) {
-                const int rr = i / per, d = (i - rr * per) * 4, r = r0 + rr;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < t.R && d < p.D) {
-                    const int tok = r / t.G, hh = h * t.G + (r - tok * t.G);
-                    x = *reinterpret_cast<const uint4*>(t.src + (int64_t)tok * t.ld + (int64_t)hh * p.D + d);
+        // 16 or 32 threads per row (Dp <= 64 or 128), four elements each
+        const int cols = p.Dp <= 64 ? 16 : 32, d = (tid & (cols - 1)) * 4;
+        if (d < p.Dp) {
+#pragma unroll 4
+            for (int rr = tid / cols; rr < kAttnTile; rr += kDecodeThreads / cols) {
+                const int r = r0 + rr;
+                uint32_t x[4] = {0u, 0u, 0u, 0u};
+                if (r < t.R) {
+                    const int tok = (int)fdiv32((uint32_t)r, t.fd_G), hh = h * t.G + (r - tok * t.G);
+                    const float* src = t.src + (int64_t)tok * t.ld + (int64_t)hh * p.D + d;
+                    if (vec) {
+                        if (d < p.D) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(src);
+                            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = d + i < p.D ? __float_as_uint(src[i]) : 0u;
+                    }
                 }
                 uint32_t* o = tile + rr * S + d;
-                o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-            }
-        } else {
-            for (int i = tid; i < kAttnTile * p.Dp; i += kDecodeThreads) {
-                const int rr = i / p.Dp, d = i - rr * p.Dp, r = r0 + rr;
-                uint32_t x = 0;
-                if (r < t.R && d < p.D) {
-                    const int tok = r / t.G, hh = h * t.G + (r - tok * t.G);
-                    x = __float_as_uint(t.src[(int64_t)tok * t.ld + (int64_t)hh * p.D + d]);
-                }
-                tile[rr * S + d] = x;
+                o[0] = x[0]; o[1] = x[1]; o[2] = x[2]; o[3] = x[3];
             }
         }
         __syncthreads();
@@ -79,13 +80,15 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
         }
         if (t.tr != nullptr) {
             Word* dst = t.tr + ((int64_t)h * t.Rp + r0) * p.D4;
-            for (int i = tid; i < kAttnTile * p.D4 / 2; i += kDecodeThreads) {
-                const int pair = i & 7, q = i >> 3, blk = q / p.D4, d = q - blk * p.D4;
+            const int pair = tid & 7;
+            for (int blk = 0; blk < kAttnTile / kAttnBlock; ++blk) {
                 const int rr = blk * kAttnBlock + pair * 2;
-                const Word a = attn_word(tile[rr * S + d], p.M, false, p.elo, p.ehi, lo, hi);
-                const Word b = attn_word(tile[(rr + 1) * S + d], p.M, false, p.elo, p.ehi, lo, hi);
-                *reinterpret_cast<uint4*>(dst + ((int64_t)blk * p.D4 + d) * kAttnBlock + pair * 2) =
-                    make_uint4(a.w, a.se, b.w, b.se);
+                for (int d = tid >> 3; d < p.D4; d += kDecodeThreads / 8) {
+                    const Word a = attn_word(tile[rr * S + d], p.M, false, p.elo, p.ehi, lo, hi);
+                    const Word b = attn_word(tile[(rr + 1) * S + d], p.M, false, p.elo, p.ehi, lo, hi);
+                    *reinterpret_cast<uint4*>(dst + ((int64_t)blk * p.D4 + d) * kAttnBlock + pair * 2) =
+                        make_uint4(a.w, a.se, b.w, b.se);
+                }
             }
         }
         if (t.row != nullptr) {
@@ -97,20 +100,13 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
                 *reinterpret_cast<uint4*>(dst + ((int64_t)g * t.Rp + rr) * CPW + c) = make_uint4(a.w, a.se, b.w, b.se);
             }
         }
-        if (t.flat != nullptr) {
-            Word* dst = t.flat + (int64_t)h * p.D4 * t.Fp;
-            for (int i = tid; i < kAttnTile * p.D4; i += kDecodeThreads) {
-                const int d = i / kAttnTile, rr = i & (kAttnTile - 1);
-                dst[(int64_t)d * t.Fp + r0 + rr] = attn_word(tile[rr * S + d], p.M, false, p.elo, p.ehi, lo, hi);
-            }
-        }
         if (p.o != nullptr && blockIdx.y == 1) {
             // D_i = sum_d dO_id o_id, exact products summed in 64 bits, four
             // threads per row, rounded once
             const int rr = tid >> 2, r = r0 + rr;
             double sum = 0.0;
             if (r < t.R) {
-                const int tok = r / t.G, hh = h * t.G + (r - tok * t.G);
+                const int tok = (int)fdiv32((uint32_t)r, t.fd_G), hh = h * t.G + (r - tok * t.G);
                 const float* o = p.o + (int64_t)tok * p.ldo + (int64_t)hh * p.D;
                 for (int d = tid & 3; d < p.D; d += 4) sum += (double)__uint_as_float(tile[rr * S + d]) * (double)o[d];
                 sum += __shfl_xor(sum, 1, 64);
@@ -300,7 +296,7 @@ struct Exchange {
 
     // keys 4 q .. 4 q + 3 of the step as lane operands
     template <bool SIGNED>
-    __device__ __forceinline__ void get(int q, uint32_t (&wa)[4], uint32_t (&sa)[4]) const
+    __device__ __forceinline__ void get(int q, uint32_t (&wa)[4], uint32_t (&sa)[4], uint32_t base) const
     {
         if constexpr (TAB == AT_LDS8) {
             const uint2 v = *reinterpret_cast<const uint2*>(buf + (q * kAttnTile + lane) * 8);
@@ -309,7 +305,7 @@ struct Exchange {
             for (int i = 0; i < 4; ++i) {
                 const uint32_t d = i < 2 ? v.x : v.y;
                 const uint32_t h = i & 1 ? d >> 16 : d & 0xFFFFu;
-                wa[i] = h == 0u ? 512u : (h << 1) & 0x1FEu;
+                wa[i] = base + (h == 0u ? 512u : (h << 1) & 0x1FEu);
                 sa[i] = (h << 15) & 0x7F800000u;
                 if (SIGNED) sa[i] |= (neg >> i) << 31;
             }
@@ -318,7 +314,7 @@ struct Exchange {
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                wa[i] = x[i] & 0x7FFFFFu;
+                wa[i] = (x[i] & 0x7FFFFFu) + base;
                 sa[i] = TAB == AT_NATIVE ? x[i] : x[i] & 0xFF800000u;
             }
         }
@@ -329,7 +325,7 @@ struct Exchange {
 // column c): `row` points at their Words [16 nb][16] of this wave's columns.
 template <int TAB, bool SIGNED>
 __device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Word* row, uint32_t quad, float (&acc)[1][CPW],
-                                      const unsigned char* lut)
+                                      const Table& lut)
 {
     if (nb <= 0) return;
     uint32_t wa[4], sa[4], q[2][2][UQ];
@@ -339,7 +335,7 @@ __device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Wor
     };
     const int n = nb * 4;
     load(0, 0);
-    ex.template get<SIGNED>(0, wa, sa);
+    ex.template get<SIGNED>(0, wa, sa, lut.lds);
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
         uint32_t wn[4], sn[4];
@@ -350,7 +346,7 @@ __device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Wor
         }
         const int next = min(k + 1, n - 1);
         load(4 * next, 0);
-        ex.template get<SIGNED>(next, wn, sn);
+        ex.template get<SIGNED>(next, wn, sn, lut.lds);
         {
             const uint32_t w2[2] = {wa[2], wa[3]}, s2[2] = {sa[2], sa[3]};
             fold<TAB, 2, 1>(w2, s2, q[1], acc, lut);
@@ -369,7 +365,7 @@ struct Place {
     int w, tt;                 // wave of its tile, tile of the workgroup
     Exchange<TAB> ex;
     double* each;              // [NW][64]: a value per row and wave of the tile
-    const unsigned char* lut;
+    Table lut;
 
     __device__ __forceinline__ Place(const AttnParams& p, unsigned char* lds)
     {
@@ -469,7 +465,7 @@ __device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB>& 
 // the row's maximum over all its keys comes first.
 template <int TAB>
 __device__ __forceinline__ void fwd_tile_checked(const AttnParams& p, const Row& r, const Span& sp, int h, int split, int g,
-                                                 const unsigned char* lut)
+                                                 const Table& lut)
 {
     const uint32_t quad = threadIdx.x & 3u;
     const Word* ql = p.q_lane + (int64_t)h * p.D4 * p.RQp + (int64_t)r.row * 4;
@@ -549,37 +545,61 @@ __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_fwd
     }
 }
 
-// Joins the chunks of every row: 16 lanes per row.
+// Joins the chunks of every row, L lanes per row: the lanes first hold the
+// chunks' maxima and sums, then the columns. L = 64 for more than 16 chunks
+// (43 chunks of 512 rows: 178 -> 36 us), else 16 (2 chunks of 98,304 rows: 34
+// against 62 us).
+template <int L>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnJoinParams p)
 {
-    const int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);   // kv head * RQ + row
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;   // kv head * RQ + row
     const int64_t rows = (int64_t)p.K * p.RQ;
     if (at >= rows) return;
+    const int lane = threadIdx.x % L;
     const int h = (int)(at / p.RQ), row = (int)(at - (int64_t)h * p.RQ);
     const int tok = row / p.G;
     // rows of no sequence keep what they hold
     int end = 0;
-    for (int b = threadIdx.x & 15; b <= p.nseq; b += 16) end = max(end, min(max(p.cu_q[b], 0), p.total_q));
-    for (int off = 8; off > 0; off >>= 1) end = max(end, __shfl_xor(end, off, 64));
+    for (int b = lane; b <= p.nseq; b += L) end = max(end, min(max(p.cu_q[b], 0), p.total_q));
+    for (int off = L / 2; off > 0; off >>= 1) end = max(end, __shfl_xor(end, off, L));
     if (tok >= end || tok < max(0, p.cu_q[0])) return;
-    double m = -__builtin_inf(), l = 0.0;
-    for (int s = 0; s < p.splits; ++s)
+    double m = -__builtin_inf();
+    for (int s = lane; s < p.splits; s += L)
         if (p.part_l[s * rows + at] != 0.0) m = fmax(m, p.part_m[s * rows + at]);
-    for (int s = 0; s < p.splits; ++s) {
-        const double ls = p.part_l[s * rows + at];
-        if (ls != 0.0) l += __builtin_ldexp(ls, (int)fmax(p.part_m[s * rows + at] - m, -4096.0));
+    for (int off = L / 2; off > 0; off >>= 1) m = fmax(m, __shfl_xor(m, off, L));
+    double l = 0.0;
+    constexpr int N = kAttnMaxDim / L;
+    float a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = 0.0f;
+    for (int s0 = 0; s0 < p.splits; s0 += L) {
+        // this lane's chunk: its power of two, or none of it (an empty chunk)
+        const int s = s0 + lane;
+        const double ls = s < p.splits ? p.part_l[s * rows + at] : 0.0;
+        const int shift = ls != 0.0 ? (int)fmax(p.part_m[s * rows + at] - m, -4096.0) : 1;
+        double t = ls != 0.0 ? __builtin_ldexp(ls, shift) : 0.0;
+        for (int off = L / 2; off > 0; off >>= 1) t += __shfl_xor(t, off, L);
+        l += t;
+        const int n = min(L, p.splits - s0);
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const int d = __shfl(shift, j, L);
+            const float* part = p.part + ((s0 + j) * rows + at) * p.Dp;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = lane + L * i;
+                const float v = c < p.Dp && d <= 0 ? part[c] : 0.0f;
+                a[i] += __builtin_ldexpf(v, d);
+            }
+        }
     }
     const int hh = h * p.G + (row - tok * p.G);
     const float inv = l == 0.0 ? 0.0f : (float)(1.0 / l);
     float* o = p.o + (int64_t)tok * p.ldo + (int64_t)hh * p.D;
-    for (int d = threadIdx.x & 15; d < p.D; d += 16) {
-        float a = 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-            if (p.part_l[s * rows + at] != 0.0)
-                a += __builtin_ldexpf(p.part[(s * rows + at) * p.Dp + d], (int)fmax(p.part_m[s * rows + at] - m, -4096.0));
-        o[d] = a * inv;
-    }
-    if (p.lse != nullptr && (threadIdx.x & 15) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane + L * i < p.D) o[lane + L * i] = a[i] * inv;
+    if (p.lse != nullptr && lane == 0)
         p.lse[(int64_t)tok * (p.K * p.G) + hh] = l == 0.0 ? -__builtin_inff() : (float)((m + log2(l)) * 0.69314718055994530942);
 }
 
@@ -664,7 +684,7 @@ __device__ __forceinline__ void dq_tile(const AttnParams& p, const Place<TAB>& a
 
 template <int TAB>
 __device__ __forceinline__ void dq_tile_checked(const AttnParams& p, const Row& r, const Span& sp, int h, int split, int g,
-                                                const unsigned char* lut)
+                                                const Table& lut)
 {
     const uint32_t quad = threadIdx.x & 3u;
     const int64_t lane_at = (int64_t)h * p.D4 * p.RQp + (int64_t)r.row * 4, tr_at = (int64_t)h * p.TKp * p.D4;
@@ -790,7 +810,7 @@ __device__ __forceinline__ void dkv_tile(const AttnParams& p, const Place<TAB>& 
 
 template <int TAB>
 __device__ __forceinline__ void dkv_tile_checked(const AttnParams& p, const Key& k, const Span& sp, int h, int split, int g,
-                                                 const unsigned char* lut)
+                                                 const Table& lut)
 {
     const uint32_t quad = threadIdx.x & 3u;
     const int64_t lane_at = (int64_t)h * p.D4 * p.TKp + (int64_t)k.key * 4, tr_at = (int64_t)h * p.RQp * p.D4;
@@ -908,7 +928,9 @@ hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t s)
 
 hipError_t launch_join(const AttnJoinParams& p, hipStream_t s)
 {
-    attn_join_kernel<<<(unsigned)(((int64_t)p.K * p.RQ + 15) / 16), 256, 0, s>>>(p);
+    const int64_t rows = (int64_t)p.K * p.RQ;
+    if (p.splits > 16) attn_join_kernel<64><<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(p);
+    else attn_join_kernel<16><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 

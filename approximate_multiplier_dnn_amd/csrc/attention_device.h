@@ -147,13 +147,22 @@ __device__ __forceinline__ Span find_tile(const int* cu_q, int total_q, const in
 
 // ------------------------------------------------------------------ products
 
+// Where the lookups read: the table's address in LDS, or its place in global
+// memory. Lane operands carry `lds` in their offsets (one addition per operand
+// instead of one per lookup), so a lookup adds only the uniform's offset, in
+// the instruction that broadcasts it.
+struct Table {
+    const unsigned char* global;
+    uint32_t lds;
+};
+
 template <int TAB>
-__device__ __forceinline__ uint32_t table_at(const unsigned char* lut, uint32_t off)
+__device__ __forceinline__ uint32_t table_at(const Table& t, uint32_t off)
 {
     if constexpr (TAB == AT_GLOBAL)
         return *reinterpret_cast<const uint16_t __attribute__((address_space(1)))*>(
-            (const unsigned char __attribute__((address_space(1)))*)lut + off);
-    else return *reinterpret_cast<const uint16_t*>(lut + off);
+            (const unsigned char __attribute__((address_space(1)))*)t.global + off);
+    else return *(const uint16_t __attribute__((address_space(3)))*)(uintptr_t)off;
 }
 
 // Column c's w (h = 0) or se (h = 1) in every lane (col_word for any number of
@@ -171,7 +180,7 @@ __device__ __forceinline__ uint32_t uniform_word(const uint32_t (&q)[NQ], int c,
 constexpr int kAhead = 12;
 template <int TAB, int NI, int GR, int NC = CPW, int NQ = UQ>
 __device__ __forceinline__ void fold(const uint32_t (&wa)[NI], const uint32_t (&sa)[NI], const uint32_t (&q)[NI][NQ],
-                                     float (&acc)[GR][NC], const unsigned char* lut)
+                                     float (&acc)[GR][NC], const Table& lut)
 {
     if constexpr (TAB == AT_NATIVE) {
 #pragma unroll
@@ -199,7 +208,7 @@ __device__ __forceinline__ void fold(const uint32_t (&wa)[NI], const uint32_t (&
 // `cols` is clear, the sum stays as it is.
 template <int TAB, int NC, int NQ>
 __device__ __forceinline__ void fold_checked(uint32_t wa, uint32_t sa, const uint32_t (&q)[NQ], float (&acc)[NC],
-                                             const unsigned char* lut, int elo, int ehi, bool keep, uint32_t cols = 0xFFFFu)
+                                             const Table& lut, int elo, int ehi, bool keep, uint32_t cols = 0xFFFFu)
 {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -217,12 +226,12 @@ __device__ __forceinline__ void fold_checked(uint32_t wa, uint32_t sa, const uin
 // ([D4][16]). Two steps at a time, their words requested two steps ahead.
 template <int TAB>
 __device__ __forceinline__ void dot_block(const Word* lane, int64_t Rp, const Word* tr, int D4, uint32_t quad,
-                                          float (&acc)[1][CPW], const unsigned char* lut)
+                                          float (&acc)[1][CPW], const Table& lut)
 {
     uint32_t wa[2][2], sa[2][2], q[2][2][UQ];
     auto load = [&](int s, int b) {
         const uint4 w = *reinterpret_cast<const uint4*>(lane + (int64_t)(s >> 1) * Rp * 4 + (s & 1) * 2);
-        wa[b][0] = w.x; sa[b][0] = w.y; wa[b][1] = w.z; sa[b][1] = w.w;
+        wa[b][0] = w.x + lut.lds; sa[b][0] = w.y; wa[b][1] = w.z + lut.lds; sa[b][1] = w.w;
         load_uniform(tr + s * 32, quad, q[b][0]);
         load_uniform(tr + s * 32 + 16, quad, q[b][1]);
     };
@@ -241,7 +250,7 @@ __device__ __forceinline__ void dot_block(const Word* lane, int64_t Rp, const Wo
 
 template <int TAB>
 __device__ __forceinline__ void dot_block_checked(const Word* lane, int64_t Rp, const Word* tr, int D4, uint32_t quad,
-                                                  float (&acc)[CPW], const unsigned char* lut, int elo, int ehi)
+                                                  float (&acc)[CPW], const Table& lut, int elo, int ehi)
 {
 #pragma unroll
     for (int c = 0; c < CPW; ++c) acc[c] = 0.0f;
@@ -250,7 +259,7 @@ __device__ __forceinline__ void dot_block_checked(const Word* lane, int64_t Rp, 
         const uint2 w = *reinterpret_cast<const uint2*>(lane + (int64_t)(d >> 2) * Rp * 4 + (d & 3));
         uint32_t q[UQ];
         load_uniform(tr + d * CPW, quad, q);
-        fold_checked<TAB>(w.x, w.y, q, acc, lut, elo, ehi, true);
+        fold_checked<TAB>(w.x + lut.lds, w.y, q, acc, lut, elo, ehi, true);
     }
 }
 
@@ -258,7 +267,7 @@ __device__ __forceinline__ void dot_block_checked(const Word* lane, int64_t Rp, 
 // [16][16] of the block's rows). seen: bit j, whether row j counts.
 template <int TAB>
 __device__ __forceinline__ void weigh_block_checked(float (&x)[CPW], uint32_t seen, const Word* row, uint32_t quad,
-                                                    float (&acc)[CPW], const unsigned char* lut, int M, int elo, int ehi)
+                                                    float (&acc)[CPW], const Table& lut, int M, int elo, int ehi)
 {
 #pragma unroll 1
     for (int j = 0; j < CPW; ++j) {
@@ -266,7 +275,7 @@ __device__ __forceinline__ void weigh_block_checked(float (&x)[CPW], uint32_t se
         const Word w = attn_word(__float_as_uint(x[0]), M, true, elo, ehi, lo, hi);
         uint32_t q[UQ];
         load_uniform(row + j * CPW, quad, q);
-        fold_checked<TAB>(w.w, w.se, q, acc, lut, elo, ehi, (seen >> j) & 1u);
+        fold_checked<TAB>(w.w + lut.lds, w.se, q, acc, lut, elo, ehi, (seen >> j) & 1u);
 #pragma unroll
         for (int i = 0; i < CPW - 1; ++i) x[i] = x[i + 1];
     }
@@ -292,19 +301,21 @@ __device__ __forceinline__ float exp2_once(double x)
     return x >= -64.0 ? v : 0.0f;
 }
 
-// The table copy, and the lookups' base.
+// The table copy, and where the lookups read it.
 template <int TAB>
-__device__ __forceinline__ const unsigned char* stage_table(const uint16_t* lut, int M, unsigned char* lds)
+__device__ __forceinline__ Table stage_table(const uint16_t* lut, int M, unsigned char* lds)
 {
+    Table t{reinterpret_cast<const unsigned char*>(lut), 0u};
     if constexpr (TAB == AT_LDS || TAB == AT_LDS8) {
         const uint4* src = reinterpret_cast<const uint4*>(lut);
         uint4* dst = reinterpret_cast<uint4*>(lds);
         const int n16 = attn_image_bytes(M) >> 4;
-        for (int t = threadIdx.x; t < n16; t += blockDim.x) dst[t] = src[t];
+        for (int i = threadIdx.x; i < n16; i += blockDim.x) dst[i] = src[i];
         __syncthreads();
-        return lds;
+        t.lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds;
+        asm("" : "+s"(t.lds));               // kept out of the lookups' address arithmetic
     }
-    return reinterpret_cast<const unsigned char*>(lut);
+    return t;
 }
 
 template <int TAB>

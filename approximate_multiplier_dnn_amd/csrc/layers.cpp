@@ -111,6 +111,7 @@ AttnTensor tensor(const float* src, int ld, int R, int G, int Rp)
     t.ld = ld;
     t.R = R;
     t.G = G;
+    t.fd_G = amx::make_fastdiv((uint32_t)G);
     t.Rp = Rp;
     return t;
 }
@@ -317,7 +318,7 @@ extern "C" int approx_attention_paged(int nseq, int heads, int kv_heads, int dim
     p.G = heads / kv_heads;
     p.D = dim;
     p.D4 = (int)round_up(dim, 4);
-    p.Dp = dim <= 64 ? 64 : 128;
+    p.Dp = (int)round_up(dim, 16);
     p.total_q = total_q;
     p.RQ = total_q * p.G;
     p.page = page;
@@ -341,44 +342,25 @@ extern "C" int approx_attention_paged(int nseq, int heads, int kv_heads, int dim
     const int64_t want = cdiv(256 * 12 * 2, heads_blocks);
     p.chunk = (int)std::max<int64_t>(64, round_up(cdiv(keys, want), 64));
     p.splits = (int)cdiv(keys, p.chunk);
-    p.items = (int64_t)p.blocks * p.K * p.splits;
-    if (p.items >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    if ((int64_t)p.blocks * p.K * p.splits >= INT32_MAX) return APPROX_EUNSUPPORTED;
+    p.q = q;
+    p.ldq = ldq;
     p.o = o;
     p.ldo = ldo;
     p.lse = lse;
 
-    AttnDecodeParams d{};
-    d.K = p.K;
-    d.D = p.D;
-    d.D4 = p.D4;
-    d.Dp = p.Dp;
-    d.M = p.M;
-    d.elo = p.elo;
-    d.ehi = p.ehi;
-    d.count = 1;
-    // a block's columns may start at the last row: a tile of zero rows follows
-    const int Rp = (int)round_up(p.RQ, amx::kAttnTile) + amx::kAttnTile;
-    d.t[0] = tensor(q, ldq, p.RQ, p.G, Rp);
-    p.Fp = d.t[0].Fp = Rp;
     Carver c;
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < 2 && p.splits > 1; ++pass) {
         c.used = 0;
-        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
-        d.t[0].flat = c.take<Word>((int64_t)p.K * p.D4 * p.Fp);
-        if (p.splits > 1) {
-            const int64_t n = (int64_t)p.splits * p.K * p.RQ;
-            p.part0 = c.take<float>(n * p.Dp);
-            p.part_m = c.take<double>(n);
-            p.part_l = c.take<double>(n);
-        }
+        const int64_t n = (int64_t)p.splits * p.K * p.RQ;
+        p.part0 = c.take<float>(n * p.Dp);
+        p.part_m = c.take<double>(n);
+        p.part_l = c.take<double>(n);
         if (pass == 0) {
             rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
             if (rc != APPROX_OK) return rc;
         }
     }
-    p.stats = d.stats;
-    p.q_flat = d.t[0].flat;
-    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
     return amx::launch_attn_paged(p, stream) == hipSuccess ? APPROX_OK : APPROX_EHIP;
 }
 
