@@ -20,7 +20,7 @@ inline int attn_table_kind(int M) { return M == 0 ? AT_NATIVE : M <= 7 ? AT_LDS 
 
 constexpr int kAttnTile = 64;       // rows (one per lane) of a wave's item
 constexpr int kAttnBlock = 16;      // columns a wave takes at a time (uniform operands)
-constexpr int kAttnSlots = 256;     // decode workgroups per tensor, each with its exponent range
+constexpr int kAttnSlots = 512;     // decode workgroups per tensor, each with its exponent range
 constexpr int kAttnMaxDim = 128;
 constexpr int kAttnMaxSplits = 32;
 
@@ -37,13 +37,27 @@ struct AttnTensor {
     int64_t ld;          // floats between tokens
     int R, G, Rp;
     FastDiv fd_G;
+    int cache;           // 1: rows are keys in a paged cache, src its pages (AttnCache)
     Word* lane;
     Word* tr;
     Word* row;
 };
 
+// Keys of a paged cache laid out as packed keys: key j of sequence b is row
+// b * stride + j (stride a multiple of 64), and bit i of mask[row / 16] says
+// whether key 16 * (row / 16) + i has a page. Blocks of 64 rows past a
+// sequence's keys are left out.
+struct AttnCache {
+    const int* k_len;
+    const int* table;
+    int table_ld, page, num_pages, stride;
+    FastDiv fd_page, fd_stride;
+    uint16_t* mask;
+};
+
 struct AttnDecodeParams {
     AttnTensor t[4];
+    AttnCache cache;
     int count;
     int K, D, D4, Dp, M, elo, ehi;
     uint32_t* stats;     // [4][kAttnSlots]: min exponent | max exponent << 8 (255 for Inf and NaN)
@@ -59,7 +73,10 @@ struct AttnDecodeParams {
 // Attention of packed sequences. cu_q / cu_k: device offsets (nseq + 1).
 struct AttnParams {
     const int* cu_q;
-    const int* cu_k;
+    const int* cu_k;          // null: sequence b's keys are k_len[b] rows from b * k_stride on (AttnCache)
+    const int* k_len;
+    int k_stride, k_most;     // k_most: largest length
+    const uint16_t* k_mask;   // or null
     int nseq, K, G, D, D4, Dp;
     int NW, TT;               // waves of a tile (Dp / 16); tiles of a workgroup (set by the launcher)
     int total_q, total_k, RQ, RQp, TKp;

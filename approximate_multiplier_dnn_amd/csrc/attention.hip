@@ -27,10 +27,12 @@ namespace amx {
 
 // Decodes 64 rows of one kv head per step through LDS into the panels asked
 // for. Bound by HBM: 4 bytes read and 8 written per element and panel.
+// (8192 tokens of 3 x 12 heads of 64, 226 MB: DECODE_US; with 256 workgroups
+// per tensor and LDS for 128 columns, too few in flight: 66 us.)
 constexpr int kDecodeThreads = 256;
 __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeParams p)
 {
-    __shared__ uint32_t tile[kAttnTile * (kAttnMaxDim + 1)];
+    extern __shared__ uint32_t tile[];               // [64][Dp + 1]
     __shared__ int range[2 * (kDecodeThreads / 64)];
     const AttnTensor& t = p.t[blockIdx.y];
     const int tid = threadIdx.x, S = p.Dp + 1;
@@ -40,6 +42,16 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
     int lo = 255, hi = 0;
     for (int64_t item = blockIdx.x; item < (int64_t)blocks * p.K; item += gridDim.x) {
         const int h = (int)(item / blocks), r0 = (int)(item - (int64_t)h * blocks) * kAttnTile;
+        const AttnCache& ca = p.cache;
+        int j0 = 0, klen = 0;                            // a cache's block: its keys j0 .. j0 + 63
+        const int* pages = nullptr;
+        if (t.cache) {
+            const int b = (int)fdiv32((uint32_t)r0, ca.fd_stride);
+            j0 = r0 - b * ca.stride;
+            klen = min(max(ca.k_len[b], 0), ca.table_ld * ca.page);
+            if (j0 >= klen) continue;                    // uniform
+            pages = ca.table + (int64_t)b * ca.table_ld;
+        }
         __syncthreads();
         // 16 or 32 threads per row (Dp <= 64 or 128), four elements each
         const int cols = p.Dp <= 64 ? 16 : 32, d = (tid & (cols - 1)) * 4;
@@ -48,9 +60,17 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
             for (int rr = tid / cols; rr < kAttnTile; rr += kDecodeThreads / cols) {
                 const int r = r0 + rr;
                 uint32_t x[4] = {0u, 0u, 0u, 0u};
-                if (r < t.R) {
+                const float* src = nullptr;
+                if (t.cache) {
+                    const int j = j0 + rr, pg = (int)fdiv32((uint32_t)j, ca.fd_page);
+                    const int page = j < klen ? pages[pg] : -1;
+                    if (page >= 0 && page < ca.num_pages)
+                        src = t.src + (((int64_t)page * ca.page + (j - pg * ca.page)) * p.K + h) * p.D + d;
+                } else if (r < t.R) {
                     const int tok = (int)fdiv32((uint32_t)r, t.fd_G), hh = h * t.G + (r - tok * t.G);
-                    const float* src = t.src + (int64_t)tok * t.ld + (int64_t)hh * p.D + d;
+                    src = t.src + (int64_t)tok * t.ld + (int64_t)hh * p.D + d;
+                }
+                if (src != nullptr) {
                     if (vec) {
                         if (d < p.D) {
                             const uint4 v = *reinterpret_cast<const uint4*>(src);
@@ -64,6 +84,12 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
                 uint32_t* o = tile + rr * S + d;
                 o[0] = x[0]; o[1] = x[1]; o[2] = x[2]; o[3] = x[3];
             }
+        }
+        if (t.cache && h == 0 && t.tr != nullptr && tid < kAttnTile) {
+            const int j = j0 + tid, pg = (int)fdiv32((uint32_t)j, ca.fd_page);
+            const int page = j < klen ? pages[pg] : -1;
+            const uint64_t there = __ballot(page >= 0 && page < ca.num_pages);
+            if (tid < kAttnTile / kAttnBlock) ca.mask[r0 / kAttnBlock + tid] = (uint16_t)(there >> (16 * tid));
         }
         __syncthreads();
         if (t.lane != nullptr) {
@@ -198,11 +224,12 @@ __device__ __forceinline__ Row tile_row(const AttnParams& p, const Span& sp, int
 }
 
 // Which of the block's 16 keys a row sees.
-__device__ __forceinline__ uint32_t seen_keys(const Row& r, const Span& sp, int j0)
+__device__ __forceinline__ uint32_t seen_keys(const AttnParams& p, const Row& r, const Span& sp, int j0)
 {
-    if (j0 >= sp.ks && j0 + kAttnBlock <= r.lim_lo) return 0xFFFFu;
+    const uint32_t there = p.k_mask != nullptr ? p.k_mask[j0 / kAttnBlock] : 0xFFFFu;
+    if (j0 >= sp.ks && j0 + kAttnBlock <= r.lim_lo) return there;
     const int a = max(0, sp.ks - j0), n = min(max(r.lim - j0, 0), kAttnBlock);
-    return ((1u << n) - 1u) & ~((1u << a) - 1u);
+    return ((1u << n) - 1u) & ~((1u << a) - 1u) & there;
 }
 
 // NG groups of 16 columns (from group g0) of a row's result: partial, or o.
@@ -424,7 +451,7 @@ __device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB>& 
         float top = -__builtin_inff();
         if (mine) {
             dot_block<TAB>(ql, p.RQp, kt + (int64_t)kb * kAttnBlock * p.D4, p.D4, quad, s, at.lut);
-            seen = seen_keys(r, sp, kb * kAttnBlock);
+            seen = seen_keys(p, r, sp, kb * kAttnBlock);
 #pragma unroll
             for (int c = 0; c < CPW; ++c) top = fmaxf(top, (seen >> c) & 1u ? s[0][c] : -__builtin_inff());
         }
@@ -440,13 +467,12 @@ __device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB>& 
             m = mn;
         }
         if (mine) {
-#pragma unroll
-            for (int c = 0; c < CPW; ++c) {
-                const float e = exp2_once(__builtin_fma((double)s[0][c], p.c, -m));
-                s[0][c] = (seen >> c) & 1u ? e : 0.0f;
-                l += (double)s[0][c];
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);    // few temporaries at a time
-            }
+            each_of_16(s[0], [&](float v, int c) {
+                const float e = exp2_once(__builtin_fma((double)v, p.c, -m));
+                const float x = (seen >> c) & 1u ? e : 0.0f;
+                l += (double)x;
+                return x;
+            });
             at.ex.template put<false>(at.w, s[0], p.M);
         }
         __syncthreads();
@@ -477,7 +503,7 @@ __device__ __forceinline__ void fwd_tile_checked(const AttnParams& p, const Row&
     for (int kb = r.f0; kb < r.f1; ++kb) {
         float s[CPW];
         dot_block_checked<TAB>(ql, p.RQp, kt + (int64_t)kb * kAttnBlock * p.D4, p.D4, quad, s, lut, p.elo, p.ehi);
-        const uint32_t seen = seen_keys(r, sp, kb * kAttnBlock);
+        const uint32_t seen = seen_keys(p, r, sp, kb * kAttnBlock);
 #pragma unroll
         for (int c = 0; c < CPW; ++c) {
             const float v = (seen >> c) & 1u ? s[c] : -__builtin_inff();
@@ -494,7 +520,7 @@ __device__ __forceinline__ void fwd_tile_checked(const AttnParams& p, const Row&
     for (int kb = r.b0; kb < r.b1; ++kb) {
         float s[CPW];
         dot_block_checked<TAB>(ql, p.RQp, kt + (int64_t)kb * kAttnBlock * p.D4, p.D4, quad, s, lut, p.elo, p.ehi);
-        const uint32_t seen = seen_keys(r, sp, kb * kAttnBlock);
+        const uint32_t seen = seen_keys(p, r, sp, kb * kAttnBlock);
 #pragma unroll
         for (int c = 0; c < CPW; ++c) {
             const float e = exp2_once(__builtin_fma((double)s[c], p.c, -m));
@@ -513,8 +539,8 @@ __host__ __device__ constexpr int max_threads() { return 64 * (TAB == AT_LDS8 ? 
 template <int TAB>
 __host__ __device__ constexpr int min_waves() { return TAB == AT_LDS8 ? 3 : 4; }
 
-// Items: TT consecutive tiles of one kv head and chunk, the tiles from the
-// last (with a causal mask the longest) outermost.
+// Items: TT consecutive tiles (in find_tile's order: those that end their
+// sequences, with a causal mask the longest, first) of one kv head and chunk.
 template <int TAB>
 __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_fwd_kernel(AttnParams p)
 {
@@ -527,13 +553,14 @@ __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_fwd
     tensor_range(p.stats, 2, vl, vh);
     const bool fast = !p.force_checked && p.elo == 1 && range_fast<TAB>(ql, qh) && range_fast<TAB>(kl, kh) &&
                       range_fast<TAB>(vl, vh) && qh + kh <= p.smax;
-    const int groups = (p.tiles + p.TT - 1) / p.TT, heads = p.K * p.splits;
+    const int heads = p.K * p.splits;
     for (;;) {
         const int item = next_item(p.next, shared);
         if (item >= p.items) break;
-        const int gt = groups - 1 - item / heads, hs = item % heads;
+        const int gt = item / heads, hs = item % heads;
         const int h = hs % p.K, split = hs / p.K;
-        Span sp = find_tile(p.cu_q, p.total_q, p.cu_k, p.total_k, p.nseq, false, p.G, kAttnTile, gt * p.TT + at.tt);
+        const Span sp = find_tile(p.cu_q, p.total_q, p.cu_k, p.total_k, p.nseq, false, p.G, kAttnTile, gt * p.TT + at.tt,
+                                  p.k_len, p.k_stride, p.k_most);
         const bool live = sp.tile >= 0;
         const Row r = tile_row(p, sp, split);
         if (!fast) {
@@ -665,14 +692,14 @@ __device__ __forceinline__ void dq_tile(const AttnParams& p, const Place<TAB>& a
             const int64_t tr = tr_at + (int64_t)kb * kAttnBlock * p.D4;
             dot_block<TAB>(p.q_lane + lane_at, p.RQp, p.k_tr + tr, p.D4, quad, s, at.lut);
             dot_block<TAB>(p.do_lane + lane_at, p.RQp, p.v_tr + tr, p.D4, quad, dp, at.lut);
-            const uint32_t seen = seen_keys(r, sp, kb * kAttnBlock);
-#pragma unroll
-            for (int c = 0; c < CPW; ++c) {
+            const uint32_t seen = seen_keys(p, r, sp, kb * kAttnBlock);
+            each_of_16(s[0], [&](float v, int c) {
                 float pr, ds;
-                score_gradient<false>(__builtin_fma((double)s[0][c], p.c, -b.base), b.lse, dp[0][c], b.delta, pr, ds);
-                s[0][c] = (seen >> c) & 1u ? ds : 0.0f;
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);    // few temporaries at a time
-            }
+                score_gradient<false>(__builtin_fma((double)v, p.c, -b.base), b.lse, dp[0][0], b.delta, pr, ds);
+#pragma unroll
+                for (int i = 0; i < CPW - 1; ++i) dp[0][i] = dp[0][i + 1];
+                return (seen >> c) & 1u ? ds : 0.0f;
+            });
         }
         __syncthreads();                     // the last step's weights have been read
         if (mine) at.ex.template put<true>(at.w, s[0], p.M);
@@ -699,7 +726,7 @@ __device__ __forceinline__ void dq_tile_checked(const AttnParams& p, const Row& 
         const int64_t tr = tr_at + (int64_t)kb * kAttnBlock * p.D4;
         dot_block_checked<TAB>(p.q_lane + lane_at, p.RQp, p.k_tr + tr, p.D4, quad, s, lut, p.elo, p.ehi);
         dot_block_checked<TAB>(p.do_lane + lane_at, p.RQp, p.v_tr + tr, p.D4, quad, dp, lut, p.elo, p.ehi);
-        const uint32_t seen = seen_keys(r, sp, kb * kAttnBlock);
+        const uint32_t seen = seen_keys(p, r, sp, kb * kAttnBlock);
 #pragma unroll
         for (int c = 0; c < CPW; ++c) {
             float pr, ds;
@@ -780,17 +807,17 @@ __device__ __forceinline__ void dkv_tile(const AttnParams& p, const Place<TAB>& 
             const uint32_t seen = seeing_rows(p, sp, k, rb * kAttnBlock);
             const float* lse_at = p.rowlse + (int64_t)h * p.RQp + rb * kAttnBlock;
             const float* delta_at = p.delta + (int64_t)h * p.RQp + rb * kAttnBlock;
-#pragma unroll
-            for (int c = 0; c < CPW; ++c) {
+            each_of_16(s[0], [&](float v, int c) {
                 const float lse = lse_at[c];
                 float pr, ds;
-                score_gradient<false>(__builtin_fma((double)s[0][c], p.c, -((double)lse * 1.4426950408889634074)), lse, dp[0][c],
+                score_gradient<false>(__builtin_fma((double)v, p.c, -((double)lse * 1.4426950408889634074)), lse, dp[0][0],
                                       delta_at[c], pr, ds);
                 const bool in = (seen >> c) & 1u;
-                s[0][c] = in ? pr : 0.0f;
-                dp[0][c] = in ? ds : 0.0f;
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);    // few temporaries at a time
-            }
+#pragma unroll
+                for (int i = 0; i < CPW - 1; ++i) dp[0][i] = dp[0][i + 1];
+                dp[0][CPW - 1] = in ? ds : 0.0f;
+                return in ? pr : 0.0f;
+            });
         }
         const int nb = min(NW, k.b1 - rb0);
         const int64_t first = row_at + (int64_t)rb0 * kAttnBlock * CPW;
@@ -845,8 +872,7 @@ __device__ __forceinline__ void dkv_tile_checked(const AttnParams& p, const Key&
     }
 }
 
-// KEYS: dK and dV (tiles of keys, from the first: with a causal mask those
-// with the most rows), else dQ (tiles of rows, from the last).
+// KEYS: dK and dV (tiles of keys), else dQ (tiles of rows).
 template <int TAB, bool KEYS>
 __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_bwd_kernel(AttnParams p)
 {
@@ -861,11 +887,11 @@ __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_bwd
         fast = fast && range_fast<TAB>(lo[t], hi[t]);
     }
     fast = fast && hi[0] + hi[2] <= p.smax;
-    const int groups = (p.tiles + p.TT - 1) / p.TT, heads = p.K * p.splits;
+    const int heads = p.K * p.splits;
     for (;;) {
         const int item = next_item(p.next, shared);
         if (item >= p.items) break;
-        const int gi = item / heads, hs = item % heads, gt = KEYS ? gi : groups - 1 - gi;
+        const int gt = item / heads, hs = item % heads;
         const int h = hs % p.K, split = hs / p.K;
         const Span sp = find_tile(p.cu_q, p.total_q, p.cu_k, p.total_k, p.nseq, KEYS, KEYS ? 1 : p.G, kAttnTile, gt * p.TT + at.tt);
         const bool live = sp.tile >= 0;
@@ -922,7 +948,7 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(SumParams p)
 
 hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t s)
 {
-    attn_decode_kernel<<<dim3(kAttnSlots, p.count), kDecodeThreads, 0, s>>>(p);
+    attn_decode_kernel<<<dim3(kAttnSlots, p.count), kDecodeThreads, kAttnTile * (p.Dp + 1) * sizeof(uint32_t), s>>>(p);
     return hipGetLastError();
 }
 

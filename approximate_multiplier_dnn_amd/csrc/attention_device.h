@@ -101,11 +101,16 @@ __device__ __forceinline__ int wave_prefix_sum(int v)
 }
 
 // Sequence and tile of tile number t when every sequence's `units` rows
-// (queries: tokens * mult; keys: tokens) are cut into tiles of `size`.
+// (queries: tokens * mult; keys: tokens) are cut into tiles of `size`. Up to
+// 64 sequences: tiles are numbered by their rank in the sequence, rows from
+// the last tile and keys from the first (with a causal mask the longest), so
+// that the longest tiles come first and short ones end the launch; more
+// sequences: one after the other.
 // Offsets are clamped to the tensors and to their running maximum, so
 // whatever they hold, sequences stay inside and do not overlap.
 __device__ __forceinline__ Span find_tile(const int* cu_q, int total_q, const int* cu_k, int total_k, int nseq,
-                                          bool by_key, int mult, int size, int t)
+                                          bool by_key, int mult, int size, int t, const int* k_len = nullptr, int k_stride = 0,
+                                          int k_most = 0)
 {
     const int lane = threadIdx.x & 63;
     int cq = 0, ck = 0, base = 0;
@@ -117,30 +122,65 @@ __device__ __forceinline__ Span find_tile(const int* cu_q, int total_q, const in
         const int bq = min(b, nseq), b1 = min(b + 1, nseq);
         const int qs = max(cq, wave_prefix_max(min(max(cu_q[bq], 0), total_q)));
         const int qe = max(qs, min(max(cu_q[b1], 0), total_q));
-        const int ks = max(ck, wave_prefix_max(min(max(cu_k[bq], 0), total_k)));
-        const int ke = max(ks, min(max(cu_k[b1], 0), total_k));
+        int ks, ke;
+        if (k_len != nullptr) {                         // fixed places, a length each
+            ks = bq * k_stride;
+            ke = ks + (b < nseq ? min(max(k_len[b], 0), k_most) : 0);
+        } else {
+            ks = max(ck, wave_prefix_max(min(max(cu_k[bq], 0), total_k)));
+            ke = max(ks, min(max(cu_k[b1], 0), total_k));
+        }
         const int n = by_key ? ke - ks : qe - qs;
         const int tiles = b < nseq ? (n * mult + size - 1) / size : 0;
-        const int incl = base + wave_prefix_sum(tiles);
-        const uint64_t found = __ballot(incl > t);
-        if (found) {
-            const int l = __builtin_ctzll(found);
+        int l = -1;
+        if (nseq <= 64) {
+            // ranks 0, 1, ... of the sequences that have so many tiles
+            int left = t, rank = 0;
+            for (;; ++rank) {
+                const uint64_t have = __ballot(tiles > rank);
+                const int count = __builtin_popcountll(have);
+                if (count == 0) break;
+                if (count == 1) {                       // one sequence: its other tiles in a step
+                    const int only = __builtin_ctzll(have);
+                    rank += left;
+                    l = rank < __shfl(tiles, only, 64) ? only : -1;
+                    break;
+                }
+                if (left < count) {                     // the left-th of these sequences
+                    uint64_t rest = have;
+                    for (int i = 0; i < left; ++i) rest &= rest - 1;
+                    l = __builtin_ctzll(rest);
+                    break;
+                }
+                left -= count;
+            }
+            if (l < 0) break;
+            sp.tile = by_key ? rank : __shfl(tiles, l, 64) - 1 - rank;
+        } else {
+            const int incl = base + wave_prefix_sum(tiles);
+            const uint64_t found = __ballot(incl > t);
+            if (found) {
+                l = __builtin_ctzll(found);
+                sp.tile = t - (__shfl(incl, l, 64) - __shfl(tiles, l, 64));
+            }
+            base = __shfl(incl, 63, 64);
+        }
+        if (l >= 0) {
             sp.seq = b0 + l;
             sp.qs = __shfl(qs, l, 64);
             sp.qn = __shfl(qe, l, 64) - sp.qs;
             sp.ks = __shfl(ks, l, 64);
             sp.kn = __shfl(ke, l, 64) - sp.ks;
-            sp.tile = t - (__shfl(incl, l, 64) - __shfl(tiles, l, 64));
             break;
         }
         cq = __shfl(qe, 63, 64);
         ck = __shfl(ke, 63, 64);
-        base = __shfl(incl, 63, 64);
     }
     sp.qs = __builtin_amdgcn_readfirstlane(sp.qs);
     sp.qn = __builtin_amdgcn_readfirstlane(sp.qn);
     sp.ks = __builtin_amdgcn_readfirstlane(sp.ks);
     sp.kn = __builtin_amdgcn_readfirstlane(sp.kn);
+    sp.seq = __builtin_amdgcn_readfirstlane(sp.seq);
     sp.tile = __builtin_amdgcn_readfirstlane(sp.tile);
     return sp;
 }
@@ -299,6 +339,24 @@ __device__ __forceinline__ float exp2_once(double x)
     r = __builtin_fma(r, f, 1.0);
     const float v = __builtin_ldexpf((float)r, (int)n);
     return x >= -64.0 ? v : 0.0f;
+}
+
+// f(element, its place) over a block's 16 values, in a loop of four (rotating
+// the registers) rather than unrolled: straight-line code runs at the speed
+// of its fetch the first time, which a short prompt's launch is made of.
+template <typename F>
+__device__ __forceinline__ void each_of_16(float (&x)[CPW], F f)
+{
+#pragma unroll 1
+    for (int g = 0; g < CPW; g += 4) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = f(x[i], g + i);
+#pragma unroll
+        for (int i = 0; i < CPW - 4; ++i) x[i] = x[i + 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[CPW - 4 + i] = y[i];
+    }
 }
 
 // The table copy, and where the lookups read it.

@@ -21,6 +21,12 @@ using amx::Word;
 
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+// Rows per sequence (tokens x heads of a group) from which a paged call
+// decodes the cache into panels for the packed kernel, and the panels' limit.
+// Four chunks of 128 tokens (256 rows) over up to 4000 keys: 510 us in blocks
+// of 16 rows, PANEL_US in panels.
+constexpr int64_t kPanelRows = 24;
+constexpr int64_t kPanelBytes = (int64_t)4 << 30;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
@@ -127,6 +133,46 @@ void fill_decode(AttnDecodeParams& d, const AttnParams& p)
     d.ehi = p.ehi;
 }
 
+// The packed forward pass: p's geometry and outputs, d's three tensors.
+// blocks: 16-key blocks of an average sequence.
+int run_forward(AttnParams& p, AttnDecodeParams& d, int64_t blocks, const HostTable& t, hipStream_t stream)
+{
+    p.lut = t.lane_first;
+    p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + p.nseq);
+    p.splits = split_for(cdiv(p.RQ, amx::kAttnTile) * p.K, blocks, p.NW);
+    if ((int64_t)p.tiles * p.K * p.splits >= INT32_MAX / 2) return APPROX_EUNSUPPORTED;
+    fill_decode(d, p);
+    d.count = 3;
+    Carver c;
+    for (int pass = 0; pass < 2; ++pass) {
+        c.used = 0;
+        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
+        d.next = c.take<int>(2);
+        d.t[0].lane = panel(c, p, p.RQp, LANE);
+        d.t[1].tr = panel(c, p, p.TKp, TR);
+        d.t[2].row = panel(c, p, p.TKp, ROW);
+        if (d.t[1].cache) d.cache.mask = c.take<uint16_t>(p.TKp / amx::kAttnBlock);
+        if (p.splits > 1) {
+            const int64_t rows = (int64_t)p.splits * p.K * p.RQ;
+            p.part0 = c.take<float>(rows * p.Dp);
+            p.part_m = c.take<double>(rows);
+            p.part_l = c.take<double>(rows);
+        }
+        if (pass == 0) {
+            const int rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
+            if (rc != APPROX_OK) return rc;
+        }
+    }
+    p.stats = d.stats;
+    p.next = d.next;
+    p.q_lane = d.t[0].lane;
+    p.k_tr = d.t[1].tr;
+    p.v_row = d.t[2].row;
+    p.k_mask = d.cache.mask;
+    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
+    return amx::launch_attn_fwd(p, stream) == hipSuccess ? APPROX_OK : APPROX_EHIP;
+}
+
 }  // namespace
 
 extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
@@ -151,46 +197,14 @@ extern "C" int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, 
 
     AttnParams p{};
     fill_common(p, Shape{nseq, heads, kv_heads, dim, total_q, total_k, causal, scale, cu_q, cu_k}, t);
-    p.lut = t.lane_first;
-    p.tiles = (int)(cdiv(p.RQ, amx::kAttnTile) + nseq);
-    p.splits = split_for((int64_t)cdiv(p.RQ, amx::kAttnTile) * p.K, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq), p.NW);
-    if ((int64_t)p.tiles * p.K * p.splits >= INT32_MAX / 2) return APPROX_EUNSUPPORTED;
     p.o = o;
     p.ldo = ldo;
     p.lse = lse;
-
     AttnDecodeParams d{};
-    fill_decode(d, p);
-    d.count = 3;
     d.t[0] = tensor(q, ldq, p.RQ, p.G, p.RQp);
     d.t[1] = tensor(k, ldk, total_k, 1, p.TKp);
     d.t[2] = tensor(v, ldv, total_k, 1, p.TKp);
-    Carver c;
-    for (int pass = 0; pass < 2; ++pass) {
-        c.used = 0;
-        d.stats = c.take<uint32_t>(4 * amx::kAttnSlots);
-        d.next = c.take<int>(2);
-        d.t[0].lane = panel(c, p, p.RQp, LANE);
-        d.t[1].tr = panel(c, p, p.TKp, TR);
-        d.t[2].row = panel(c, p, p.TKp, ROW);
-        if (p.splits > 1) {
-            const int64_t rows = (int64_t)p.splits * p.K * p.RQ;
-            p.part0 = c.take<float>(rows * p.Dp);
-            p.part_m = c.take<double>(rows);
-            p.part_l = c.take<double>(rows);
-        }
-        if (pass == 0) {
-            rc = amx::host_scratch(t.dev, stream, c.used, &c.base);
-            if (rc != APPROX_OK) return rc;
-        }
-    }
-    p.stats = d.stats;
-    p.next = d.next;
-    p.q_lane = d.t[0].lane;
-    p.k_tr = d.t[1].tr;
-    p.v_row = d.t[2].row;
-    if (amx::launch_attn_decode(d, stream) != hipSuccess) return APPROX_EHIP;
-    return amx::launch_attn_fwd(p, stream) == hipSuccess ? APPROX_OK : APPROX_EHIP;
+    return run_forward(p, d, cdiv(total_k, (int64_t)amx::kAttnBlock * nseq), t, stream);
 }
 
 extern "C" int approx_attention_bwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,
@@ -307,6 +321,36 @@ extern "C" int approx_attention_paged(int nseq, int heads, int kv_heads, int dim
     if (rc != APPROX_OK) return rc;
     hipStream_t stream = static_cast<hipStream_t>(stream_v);
 
+    const int64_t rows = cdiv(total_q, nseq) * (heads / kv_heads);   // of an average sequence
+    const int64_t stride = round_up((int64_t)table_ld * page, amx::kAttnTile), all = nseq * stride;
+    const int64_t panels = all * kv_heads * (round_up(dim, 4) + round_up(dim, 16)) * (int64_t)sizeof(Word);
+    if (rows >= kPanelRows && table_ld > 0 && all < kMaxRows && panels <= kPanelBytes) {
+        // chunks: the cache's keys decoded once for all the rows, then the
+        // packed forward pass
+        AttnParams p{};
+        fill_common(p, Shape{nseq, heads, kv_heads, dim, total_q, (int)all, causal, scale, cu_q, nullptr}, t);
+        p.k_len = k_len;
+        p.k_stride = (int)stride;
+        p.k_most = table_ld * page;
+        p.o = o;
+        p.ldo = ldo;
+        p.lse = lse;
+        AttnDecodeParams d{};
+        d.t[0] = tensor(q, ldq, p.RQ, p.G, p.RQp);
+        d.t[1] = tensor(k_pages, dim * 4, (int)all, 1, p.TKp);
+        d.t[2] = tensor(v_pages, dim * 4, (int)all, 1, p.TKp);
+        d.t[1].cache = d.t[2].cache = 1;
+        d.cache.k_len = k_len;
+        d.cache.table = block_table;
+        d.cache.table_ld = table_ld;
+        d.cache.page = page;
+        d.cache.num_pages = num_pages;
+        d.cache.stride = (int)stride;
+        d.cache.fd_page = amx::make_fastdiv((uint32_t)page);
+        d.cache.fd_stride = amx::make_fastdiv((uint32_t)stride);
+        return run_forward(p, d, stride / amx::kAttnBlock, t, stream);
+    }
+
     amx::PagedParams p{};
     p.cu_q = cu_q;
     p.k_len = k_len;
@@ -334,13 +378,13 @@ extern "C" int approx_attention_paged(int nseq, int heads, int kv_heads, int dim
     p.smax = score_limit(p.c);
     p.force_checked = t.force_checked;
     p.lut = t.uniform_first;
-    const int64_t rows = cdiv(total_q, nseq) * p.G;         // of an average sequence
     p.NR = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
     p.blocks = (int)(cdiv(p.RQ, p.NR) + nseq);
     const int64_t keys = std::max<int64_t>(1, (int64_t)table_ld * page);
     const int64_t heads_blocks = std::max<int64_t>(1, std::max<int64_t>(cdiv(p.RQ, p.NR), nseq) * p.K);
     const int64_t want = cdiv(256 * 12 * 2, heads_blocks);
-    p.chunk = (int)std::max<int64_t>(64, round_up(cdiv(keys, want), 64));
+    // 64 keys fill a wave; 32 when there are few items (a wave's time per item counts then)
+    p.chunk = cdiv(keys, want) <= 32 ? 32 : (int)round_up(cdiv(keys, want), 64);
     p.splits = (int)cdiv(keys, p.chunk);
     if ((int64_t)p.blocks * p.K * p.splits >= INT32_MAX) return APPROX_EUNSUPPORTED;
     p.q = q;
