@@ -21,6 +21,8 @@
 // product), as in the GEMM kernel.
 #include "attention_device.h"
 
+#include <cstdlib>
+
 namespace amx {
 
 // ------------------------------------------------------------------ decode
@@ -165,23 +167,20 @@ __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeP
 
 // ------------------------------------------------------------------ tiles
 
-// One row of 16 DC sums: scaled into the output, or as a partial.
-template <int DC>
-__device__ __forceinline__ void store_row(const float (&acc)[DC][CPW], float scale, float* o, int D, bool vec)
+// CW sums of a row: scaled into the output (its columns below D), or as a partial.
+template <int CW>
+__device__ __forceinline__ void store_row(const float (&acc)[1][CW], float scale, float* o, int D, bool vec)
 {
 #pragma unroll
-    for (int g = 0; g < DC; ++g)
+    for (int d = 0; d < CW; d += 4) {
+        if (vec) {
+            if (d < D) *reinterpret_cast<float4*>(o + d) = make_float4(acc[0][d] * scale, acc[0][d + 1] * scale, acc[0][d + 2] * scale, acc[0][d + 3] * scale);
+        } else {
 #pragma unroll
-        for (int c = 0; c < CPW; c += 4) {
-            const int d = g * CPW + c;
-            if (vec) {
-                if (d < D) *reinterpret_cast<float4*>(o + d) = make_float4(acc[g][c] * scale, acc[g][c + 1] * scale, acc[g][c + 2] * scale, acc[g][c + 3] * scale);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (d + x < D) o[d + x] = acc[g][c + x] * scale;
-            }
+            for (int x = 0; x < 4; ++x)
+                if (d + x < D) o[d + x] = acc[0][d + x] * scale;
         }
+    }
 }
 
 __device__ __forceinline__ bool rows_aligned(const float* o, int64_t ld, int D)
@@ -232,23 +231,22 @@ __device__ __forceinline__ uint32_t seen_keys(const AttnParams& p, const Row& r,
     return ((1u << n) - 1u) & ~((1u << a) - 1u) & there;
 }
 
-// NG groups of 16 columns (from group g0) of a row's result: partial, or o.
-template <int NG>
-__device__ __forceinline__ void store_fwd(const AttnParams& p, const Row& r, int h, int split, int g0,
-                                          const float (&acc)[NG][CPW], double m, double l)
+// CW columns (from CW g on) of a row's result: partial, or o.
+template <int CW>
+__device__ __forceinline__ void store_fwd(const AttnParams& p, const Row& r, int h, int split, int g, const float (&acc)[1][CW],
+                                          double m, double l)
 {
     if (!r.valid) return;
     if (p.splits > 1) {
         const int64_t at = ((int64_t)split * p.K + h) * p.RQ + r.row;
         p.part_m[at] = m;
         p.part_l[at] = l;
-        if (l != 0.0) store_row<NG>(acc, 1.0f, p.part0 + at * p.Dp + g0 * CPW, p.Dp - g0 * CPW, true);
+        if (l != 0.0) store_row(acc, 1.0f, p.part0 + at * p.Dp + g * CW, CW, true);
         return;
     }
     const int hh = h * p.G + (r.row - r.tok * p.G);
     const float inv = l == 0.0 ? 0.0f : (float)(1.0 / l);
-    store_row<NG>(acc, inv, p.o + (int64_t)r.tok * p.ldo + (int64_t)hh * p.D + g0 * CPW, p.D - g0 * CPW,
-                  rows_aligned(p.o, p.ldo, p.D));
+    store_row(acc, inv, p.o + (int64_t)r.tok * p.ldo + (int64_t)hh * p.D + g * CW, p.D - g * CW, rows_aligned(p.o, p.ldo, p.D));
     if (p.lse != nullptr)
         p.lse[(int64_t)r.tok * (p.K * p.G) + hh] = l == 0.0 ? -__builtin_inff() : (float)((m + log2(l)) * 0.69314718055994530942);
 }
@@ -269,16 +267,16 @@ __device__ __forceinline__ void store_fwd(const AttnParams& p, const Row& r, int
 // Exchange of a step's weights: [key / 4][row][4] words of sign | exponent bits
 // and row offset (disjoint bits; the floats themselves with the native
 // multiplier). At M = 8, whose table leaves no room for that, exponent and
-// mantissa index in 16 bits, and the signs of 16 keys in one 16-bit mask.
+// mantissa index in 16 bits, and the signs of 8 keys in one byte.
 template <int TAB>
 __host__ __device__ constexpr int exchange_bytes(int NW)
 {
     return TAB == AT_LDS8 ? NW * (16 * kAttnTile * 2 + kAttnTile * 2) : NW * 16 * kAttnTile * 4;
 }
 template <int TAB>
-__host__ __device__ constexpr int tile_bytes(int NW)
+__host__ __device__ constexpr int tile_bytes(int NW, int CW)
 {
-    return exchange_bytes<TAB>(NW) + NW * kAttnTile * 8;        // + a double per row and wave
+    return exchange_bytes<TAB>(NW) + NW * (16 / CW) * kAttnTile * 8;        // + a double per row and wave
 }
 
 template <int TAB>
@@ -286,16 +284,16 @@ struct Exchange {
     unsigned char* buf;
     int NW, lane;
 
-    __device__ __forceinline__ uint16_t* signs() const { return reinterpret_cast<uint16_t*>(buf + NW * 16 * kAttnTile * 2); }
+    __device__ __forceinline__ uint8_t* signs() const { return buf + NW * 16 * kAttnTile * 2; }
 
-    // wave w's 16 weights of this lane's row
-    template <bool SIGNED>
-    __device__ __forceinline__ void put(int w, const float (&x)[CPW], int M) const
+    // wave w's CW weights of this lane's row
+    template <bool SIGNED, int CW>
+    __device__ __forceinline__ void put(int w, const float (&x)[CW], int M) const
     {
         if constexpr (TAB == AT_LDS8) {
             uint32_t neg = 0u;
 #pragma unroll
-            for (int j = 0; j < CPW; j += 4) {
+            for (int j = 0; j < CW; j += 4) {
                 uint32_t h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -303,12 +301,14 @@ struct Exchange {
                     h[i] = (b << 1) >> 16;
                     if (SIGNED) neg |= (b >> 31) << (j + i);
                 }
-                *reinterpret_cast<uint2*>(buf + ((w * 4 + j / 4) * kAttnTile + lane) * 8) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+                *reinterpret_cast<uint2*>(buf + (((w * CW + j) / 4) * kAttnTile + lane) * 8) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
             }
-            if (SIGNED) signs()[w * kAttnTile + lane] = (uint16_t)neg;
+            if (SIGNED)
+#pragma unroll
+                for (int j = 0; j < CW; j += 8) signs()[((w * CW + j) / 8) * kAttnTile + lane] = (uint8_t)(neg >> j);
         } else {
 #pragma unroll
-            for (int j = 0; j < CPW; j += 4) {
+            for (int j = 0; j < CW; j += 4) {
                 uint32_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -316,7 +316,7 @@ struct Exchange {
                     const uint32_t o = b << 1 == 0u ? (2u << M) : (b >> (22 - M)) & ((2u << M) - 2u);
                     v[i] = TAB == AT_NATIVE ? b : (b & 0xFF800000u) | o;
                 }
-                *reinterpret_cast<uint4*>(buf + ((w * 4 + j / 4) * kAttnTile + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(buf + (((w * CW + j) / 4) * kAttnTile + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
     }
@@ -327,7 +327,7 @@ struct Exchange {
     {
         if constexpr (TAB == AT_LDS8) {
             const uint2 v = *reinterpret_cast<const uint2*>(buf + (q * kAttnTile + lane) * 8);
-            const uint32_t neg = SIGNED ? (uint32_t)signs()[(q >> 2) * kAttnTile + lane] >> ((q & 3) * 4) : 0u;
+            const uint32_t neg = SIGNED ? (uint32_t)signs()[(q >> 1) * kAttnTile + lane] >> ((q & 1) * 4) : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t d = i < 2 ? v.x : v.y;
@@ -349,16 +349,15 @@ struct Exchange {
 };
 
 // acc[0][c] += sum over the step's first 16 nb rows j of T(weight j, row j's
-// column c): `row` points at their Words [16 nb][16] of this wave's columns.
-template <int TAB, bool SIGNED>
-__device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Word* row, uint32_t quad, float (&acc)[1][CPW],
-                                      const Table& lut)
+// column c): `row` points at this wave's columns of their Words [16 nb][16].
+template <int TAB, bool SIGNED, int CW>
+__device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Word* row, float (&acc)[1][CW], const Table& lut)
 {
     if (nb <= 0) return;
-    uint32_t wa[4], sa[4], q[2][2][UQ];
+    uint32_t wa[4], sa[4], q[2][2][CW / 2];
     auto load = [&](int j, int b) {
-        load_uniform(row + j * CPW, quad, q[b][0]);
-        load_uniform(row + (j + 1) * CPW, quad, q[b][1]);
+        load_columns(row + j * 16, q[b][0]);
+        load_columns(row + (j + 1) * 16, q[b][1]);
     };
     const int n = nb * 4;
     load(0, 0);
@@ -369,14 +368,14 @@ __device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Wor
         load(4 * k + 2, 1);
         {
             const uint32_t w2[2] = {wa[0], wa[1]}, s2[2] = {sa[0], sa[1]};
-            fold<TAB, 2, 1>(w2, s2, q[0], acc, lut);
+            fold<TAB, 2, 1, CW, CW / 2>(w2, s2, q[0], acc, lut);
         }
         const int next = min(k + 1, n - 1);
         load(4 * next, 0);
         ex.template get<SIGNED>(next, wn, sn, lut.lds);
         {
             const uint32_t w2[2] = {wa[2], wa[3]}, s2[2] = {sa[2], sa[3]};
-            fold<TAB, 2, 1>(w2, s2, q[1], acc, lut);
+            fold<TAB, 2, 1, CW, CW / 2>(w2, s2, q[1], acc, lut);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -386,24 +385,31 @@ __device__ __forceinline__ void weigh(const Exchange<TAB>& ex, int nb, const Wor
     }
 }
 
-// This wave's place in its workgroup.
-template <int TAB>
+// This wave's place in its workgroup: wave w of tile tt takes CW keys of a
+// step and CW columns: block w CW / 16 of the step's 16-key blocks (and column
+// group), from position `off` in it.
+template <int TAB, int CW>
 struct Place {
-    int w, tt;                 // wave of its tile, tile of the workgroup
+    int w, tt, waves, blk, off;
     Exchange<TAB> ex;
-    double* each;              // [NW][64]: a value per row and wave of the tile
+    double* each;              // [waves][64]: a value per row and wave of the tile
     Table lut;
 
     __device__ __forceinline__ Place(const AttnParams& p, unsigned char* lds)
     {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);    // in scalar registers
-        tt = wave / p.NW;
-        w = wave - tt * p.NW;
-        unsigned char* at = lds + table_lds<TAB>() + 64 + tt * tile_bytes<TAB>(p.NW);
+        waves = p.NW * (16 / CW);
+        tt = wave / waves;
+        w = wave - tt * waves;
+        blk = w * CW / 16;
+        off = w * CW % 16;
+        unsigned char* at = lds + table_lds<TAB>() + 64 + tt * tile_bytes<TAB>(p.NW, CW);
         ex = Exchange<TAB>{at, p.NW, (int)(threadIdx.x & 63)};
         each = reinterpret_cast<double*>(at + exchange_bytes<TAB>(p.NW));
         lut = stage_table<TAB>(p.lut, p.M, lds);
     }
+    // which of this wave's keys (rows) of a block count
+    __device__ __forceinline__ uint32_t part(uint32_t seen) const { return (seen >> off) & ((1u << CW) - 1u); }
 };
 
 // The workgroup's next TT tiles: an item number from the counter, through LDS.
@@ -428,46 +434,45 @@ __device__ __forceinline__ int most_steps(int steps, int tt, int TT, int* shared
 
 // ------------------------------------------------------------------ forward
 
-template <int TAB>
-__device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB>& at, const Row& r, const Span& sp, bool live, int h,
+template <int TAB, int CW>
+__device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB, CW>& at, const Row& r, const Span& sp, bool live, int h,
                                          int split, int steps)
 {
-    const uint32_t quad = threadIdx.x & 3u;
     const int lane = threadIdx.x & 63, NW = p.NW;
     const Word* ql = p.q_lane + (int64_t)h * p.D4 * p.RQp + (int64_t)r.row * 4;
-    const Word* kt = p.k_tr + (int64_t)h * p.TKp * p.D4;
-    const Word* vr = p.v_row + ((int64_t)h * NW + at.w) * p.TKp * CPW;
+    const Word* kt = p.k_tr + (int64_t)h * p.TKp * p.D4 + at.off;
+    const Word* vr = p.v_row + ((int64_t)h * NW + at.blk) * p.TKp * 16 + at.off;
     float* tops = reinterpret_cast<float*>(at.each);
-    float acc[1][CPW];
+    float acc[1][CW];
 #pragma unroll
-    for (int c = 0; c < CPW; ++c) acc[0][c] = 0.0f;
+    for (int c = 0; c < CW; ++c) acc[0][c] = 0.0f;
     double m = -__builtin_inf(), l = 0.0;
 #pragma unroll 1
     for (int it = 0; it < steps; ++it) {
-        const int kb0 = r.b0 + it * NW, kb = kb0 + at.w;
+        const int kb0 = r.b0 + it * NW, kb = kb0 + at.blk;
         const bool mine = live && kb < r.b1;
-        float s[1][CPW];
+        float s[1][CW];
         uint32_t seen = 0u;
         float top = -__builtin_inff();
         if (mine) {
-            dot_block<TAB>(ql, p.RQp, kt + (int64_t)kb * kAttnBlock * p.D4, p.D4, quad, s, at.lut);
-            seen = seen_keys(p, r, sp, kb * kAttnBlock);
+            dot_block<TAB, CW>(ql, p.RQp, kt + (int64_t)kb * kAttnBlock * p.D4, p.D4, s, at.lut);
+            seen = at.part(seen_keys(p, r, sp, kb * kAttnBlock));
 #pragma unroll
-            for (int c = 0; c < CPW; ++c) top = fmaxf(top, (seen >> c) & 1u ? s[0][c] : -__builtin_inff());
+            for (int c = 0; c < CW; ++c) top = fmaxf(top, (seen >> c) & 1u ? s[0][c] : -__builtin_inff());
         }
         tops[at.w * kAttnTile + lane] = top;
         __syncthreads();
-        for (int x = 0; x < NW; ++x) top = fmaxf(top, tops[x * kAttnTile + lane]);
+        for (int x = 0; x < at.waves; ++x) top = fmaxf(top, tops[x * kAttnTile + lane]);
         const double mn = fmax(m, __builtin_ceil((double)top * p.c));
         if (__any(mn > m)) {                 // a power of two: no mantissa changes
             const int d = mn > m ? (int)fmax(m - mn, -4096.0) : 0;
             l = __builtin_ldexp(l, d);
 #pragma unroll
-            for (int c = 0; c < CPW; ++c) acc[0][c] = __builtin_ldexpf(acc[0][c], d);
+            for (int c = 0; c < CW; ++c) acc[0][c] = __builtin_ldexpf(acc[0][c], d);
             m = mn;
         }
         if (mine) {
-            each_of_16(s[0], [&](float v, int c) {
+            each_value(s[0], [&](float v, int c) {
                 const float e = exp2_once(__builtin_fma((double)v, p.c, -m));
                 const float x = (seen >> c) & 1u ? e : 0.0f;
                 l += (double)x;
@@ -476,13 +481,13 @@ __device__ __forceinline__ void fwd_tile(const AttnParams& p, const Place<TAB>& 
             at.ex.template put<false>(at.w, s[0], p.M);
         }
         __syncthreads();
-        if (live) weigh<TAB, false>(at.ex, min(NW, r.b1 - kb0), vr + (int64_t)kb0 * kAttnBlock * CPW, quad, acc, at.lut);
+        if (live) weigh<TAB, false>(at.ex, min(NW, r.b1 - kb0), vr + (int64_t)kb0 * kAttnBlock * 16, acc, at.lut);
     }
     at.each[at.w * kAttnTile + lane] = l;
     __syncthreads();
     l = 0.0;
-    for (int x = 0; x < NW; ++x) l += at.each[x * kAttnTile + lane];
-    if (live) store_fwd<1>(p, r, h, split, at.w, acc, m, l);
+    for (int x = 0; x < at.waves; ++x) l += at.each[x * kAttnTile + lane];
+    if (live) store_fwd(p, r, h, split, at.w, acc, m, l);
 }
 
 // The checked path, kept small rather than fast: every wave computes all the
@@ -530,23 +535,27 @@ __device__ __forceinline__ void fwd_tile_checked(const AttnParams& p, const Row&
         weigh_block_checked<TAB>(s, seen, vr + (int64_t)kb * kAttnBlock * CPW, quad, acc[0], lut, p.M, p.elo, p.ehi);
     }
     if (bad) l = __builtin_nan("");
-    store_fwd<1>(p, r, h, split, g, acc, m, l);
+    store_fwd(p, r, h, split, g, acc, m, l);
 }
 
-constexpr int kMaxWaves = 8;                 // of a workgroup; 12 at M = 8, where one workgroup fills a CU's LDS
-template <int TAB>
-__host__ __device__ constexpr int max_threads() { return 64 * (TAB == AT_LDS8 ? 12 : kMaxWaves); }
-template <int TAB>
-__host__ __device__ constexpr int min_waves() { return TAB == AT_LDS8 ? 3 : 4; }
+// CW, the keys and columns of a wave: 16, or 8 for calls that leave the GPU
+// mostly empty (a lone wave issues one instruction in five or more clocks, so
+// twice the waves of half the work end sooner; FEW_US).
+// Waves of a workgroup: up to 8; 12 at M = 8, where one workgroup fills a CU's
+// LDS; up to 16 with CW = 8 (two per 16 columns).
+template <int TAB, int CW>
+__host__ __device__ constexpr int max_waves() { return CW == 8 ? 16 : TAB == AT_LDS8 ? 12 : 8; }
+template <int TAB, int CW>
+__host__ __device__ constexpr int min_waves() { return CW == 16 && TAB == AT_LDS8 ? 3 : 4; }
 
 // Items: TT consecutive tiles (in find_tile's order: those that end their
 // sequences, with a causal mask the longest, first) of one kv head and chunk.
-template <int TAB>
-__global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_fwd_kernel(AttnParams p)
+template <int TAB, int CW>
+__global__ __launch_bounds__((64 * max_waves<TAB, CW>()), (min_waves<TAB, CW>())) void attn_fwd_kernel(AttnParams p)
 {
     extern __shared__ __align__(16) unsigned char lds[];
     int* shared = reinterpret_cast<int*>(lds + table_lds<TAB>());
-    const Place<TAB> at(p, lds);
+    const Place<TAB, CW> at(p, lds);
     int ql, qh, kl, kh, vl, vh;
     tensor_range(p.stats, 0, ql, qh);
     tensor_range(p.stats, 1, kl, kh);
@@ -564,11 +573,11 @@ __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_fwd
         const bool live = sp.tile >= 0;
         const Row r = tile_row(p, sp, split);
         if (!fast) {
-            if (live) fwd_tile_checked<TAB>(p, r, sp, h, split, at.w, at.lut);
+            if (live && at.w < p.NW) fwd_tile_checked<TAB>(p, r, sp, h, split, at.w, at.lut);
             continue;
         }
         const int steps = most_steps(live ? (r.b1 - r.b0 + p.NW - 1) / p.NW : 0, at.tt, p.TT, shared);
-        fwd_tile<TAB>(p, at, r, sp, live, h, split, steps);
+        fwd_tile<TAB, CW>(p, at, r, sp, live, h, split, steps);
     }
 }
 
@@ -656,55 +665,55 @@ __device__ __forceinline__ RowState row_state(const AttnParams& p, const Row& r,
     return b;
 }
 
-__device__ __forceinline__ void store_dq(const AttnParams& p, const Row& r, int h, int split, int g, const float (&acc)[1][CPW])
+template <int CW>
+__device__ __forceinline__ void store_dq(const AttnParams& p, const Row& r, int h, int split, int g, const float (&acc)[1][CW])
 {
     if (!r.valid) return;
     if (p.splits > 1) {
-        store_row<1>(acc, 1.0f, p.part0 + (((int64_t)split * p.K + h) * p.RQ + r.row) * p.Dp + g * CPW, CPW, true);
+        store_row(acc, 1.0f, p.part0 + (((int64_t)split * p.K + h) * p.RQ + r.row) * p.Dp + g * CW, CW, true);
     } else {
         float* o = p.dq + (int64_t)r.tok * p.lddq + (int64_t)(h * p.G + (r.row - r.tok * p.G)) * p.D;
-        store_row<1>(acc, p.scale, o + g * CPW, p.D - g * CPW, rows_aligned(p.dq, p.lddq, p.D));
+        store_row(acc, p.scale, o + g * CW, p.D - g * CW, rows_aligned(p.dq, p.lddq, p.D));
     }
 }
 
-// dQ of 64 rows: each wave the scores and dP of 16 keys of a step and their
-// dS, then 16 columns of the sum over the step's keys.
-template <int TAB>
-__device__ __forceinline__ void dq_tile(const AttnParams& p, const Place<TAB>& at, const Row& r, const Span& sp, bool live, int h,
+// dQ of 64 rows: each wave the scores and dP of CW keys of a step and their
+// dS, then CW columns of the sum over the step's keys.
+template <int TAB, int CW>
+__device__ __forceinline__ void dq_tile(const AttnParams& p, const Place<TAB, CW>& at, const Row& r, const Span& sp, bool live, int h,
                                         int split, int steps)
 {
-    const uint32_t quad = threadIdx.x & 3u;
     const int NW = p.NW;
-    const int64_t lane_at = (int64_t)h * p.D4 * p.RQp + (int64_t)r.row * 4, tr_at = (int64_t)h * p.TKp * p.D4;
-    const Word* kr = p.k_row + ((int64_t)h * NW + at.w) * p.TKp * CPW;
+    const int64_t lane_at = (int64_t)h * p.D4 * p.RQp + (int64_t)r.row * 4, tr_at = (int64_t)h * p.TKp * p.D4 + at.off;
+    const Word* kr = p.k_row + ((int64_t)h * NW + at.blk) * p.TKp * 16 + at.off;
     RowState b{0.0f, 0.0f, 0.0};
     if (live) b = row_state(p, r, h);
-    float acc[1][CPW];
+    float acc[1][CW];
 #pragma unroll
-    for (int c = 0; c < CPW; ++c) acc[0][c] = 0.0f;
+    for (int c = 0; c < CW; ++c) acc[0][c] = 0.0f;
 #pragma unroll 1
     for (int it = 0; it < steps; ++it) {
-        const int kb0 = r.b0 + it * NW, kb = kb0 + at.w;
-        float s[1][CPW];
+        const int kb0 = r.b0 + it * NW, kb = kb0 + at.blk;
+        float s[1][CW];
         const bool mine = live && kb < r.b1;
         if (mine) {
-            float dp[1][CPW];
+            float dp[1][CW];
             const int64_t tr = tr_at + (int64_t)kb * kAttnBlock * p.D4;
-            dot_block<TAB>(p.q_lane + lane_at, p.RQp, p.k_tr + tr, p.D4, quad, s, at.lut);
-            dot_block<TAB>(p.do_lane + lane_at, p.RQp, p.v_tr + tr, p.D4, quad, dp, at.lut);
-            const uint32_t seen = seen_keys(p, r, sp, kb * kAttnBlock);
-            each_of_16(s[0], [&](float v, int c) {
+            dot_block<TAB, CW>(p.q_lane + lane_at, p.RQp, p.k_tr + tr, p.D4, s, at.lut);
+            dot_block<TAB, CW>(p.do_lane + lane_at, p.RQp, p.v_tr + tr, p.D4, dp, at.lut);
+            const uint32_t seen = at.part(seen_keys(p, r, sp, kb * kAttnBlock));
+            each_value(s[0], [&](float v, int c) {
                 float pr, ds;
                 score_gradient<false>(__builtin_fma((double)v, p.c, -b.base), b.lse, dp[0][0], b.delta, pr, ds);
 #pragma unroll
-                for (int i = 0; i < CPW - 1; ++i) dp[0][i] = dp[0][i + 1];
+                for (int i = 0; i < CW - 1; ++i) dp[0][i] = dp[0][i + 1];
                 return (seen >> c) & 1u ? ds : 0.0f;
             });
         }
         __syncthreads();                     // the last step's weights have been read
         if (mine) at.ex.template put<true>(at.w, s[0], p.M);
         __syncthreads();
-        if (live) weigh<TAB, true>(at.ex, min(NW, r.b1 - kb0), kr + (int64_t)kb0 * kAttnBlock * CPW, quad, acc, at.lut);
+        if (live) weigh<TAB, true>(at.ex, min(NW, r.b1 - kb0), kr + (int64_t)kb0 * kAttnBlock * 16, acc, at.lut);
     }
     if (live) store_dq(p, r, h, split, at.w, acc);
 }
@@ -774,61 +783,59 @@ __device__ __forceinline__ uint32_t seeing_rows(const AttnParams& p, const Span&
     return seen;
 }
 
-__device__ __forceinline__ void store_key(const AttnParams& p, const Key& k, int h, int split, int g, const float (&acc)[1][CPW],
+template <int CW>
+__device__ __forceinline__ void store_key(const AttnParams& p, const Key& k, int h, int split, int g, const float (&acc)[1][CW],
                                           float* part, float* out, int64_t ld, float scale)
 {
     if (!k.valid) return;
-    if (p.splits > 1)
-        store_row<1>(acc, 1.0f, part + (((int64_t)split * p.K + h) * p.total_k + k.key) * p.Dp + g * CPW, CPW, true);
-    else
-        store_row<1>(acc, scale, out + (int64_t)k.key * ld + (int64_t)h * p.D + g * CPW, p.D - g * CPW, rows_aligned(out, ld, p.D));
+    if (p.splits > 1) store_row(acc, 1.0f, part + (((int64_t)split * p.K + h) * p.total_k + k.key) * p.Dp + g * CW, CW, true);
+    else store_row(acc, scale, out + (int64_t)k.key * ld + (int64_t)h * p.D + g * CW, p.D - g * CW, rows_aligned(out, ld, p.D));
 }
 
-template <int TAB>
-__device__ __forceinline__ void dkv_tile(const AttnParams& p, const Place<TAB>& at, const Key& k, const Span& sp, bool live, int h,
+template <int TAB, int CW>
+__device__ __forceinline__ void dkv_tile(const AttnParams& p, const Place<TAB, CW>& at, const Key& k, const Span& sp, bool live, int h,
                                          int split, int steps)
 {
-    const uint32_t quad = threadIdx.x & 3u;
     const int NW = p.NW;
-    const int64_t lane_at = (int64_t)h * p.D4 * p.TKp + (int64_t)k.key * 4, tr_at = (int64_t)h * p.RQp * p.D4;
-    const int64_t row_at = ((int64_t)h * NW + at.w) * p.RQp * CPW;
-    float dv[1][CPW], dk[1][CPW];
+    const int64_t lane_at = (int64_t)h * p.D4 * p.TKp + (int64_t)k.key * 4, tr_at = (int64_t)h * p.RQp * p.D4 + at.off;
+    const int64_t row_at = ((int64_t)h * NW + at.blk) * p.RQp * 16 + at.off;
+    float dv[1][CW], dk[1][CW];
 #pragma unroll
-    for (int c = 0; c < CPW; ++c) dv[0][c] = dk[0][c] = 0.0f;
+    for (int c = 0; c < CW; ++c) dv[0][c] = dk[0][c] = 0.0f;
 #pragma unroll 1
     for (int it = 0; it < steps; ++it) {
-        const int rb0 = k.b0 + it * NW, rb = rb0 + at.w;
-        float s[1][CPW], dp[1][CPW];
+        const int rb0 = k.b0 + it * NW, rb = rb0 + at.blk;
+        float s[1][CW], dp[1][CW];
         const bool mine = live && rb < k.b1;
         if (mine) {
             const int64_t tr = tr_at + (int64_t)rb * kAttnBlock * p.D4;
-            dot_block<TAB>(p.k_lane + lane_at, p.TKp, p.q_tr + tr, p.D4, quad, s, at.lut);
-            dot_block<TAB>(p.v_lane + lane_at, p.TKp, p.do_tr + tr, p.D4, quad, dp, at.lut);
-            const uint32_t seen = seeing_rows(p, sp, k, rb * kAttnBlock);
-            const float* lse_at = p.rowlse + (int64_t)h * p.RQp + rb * kAttnBlock;
-            const float* delta_at = p.delta + (int64_t)h * p.RQp + rb * kAttnBlock;
-            each_of_16(s[0], [&](float v, int c) {
+            dot_block<TAB, CW>(p.k_lane + lane_at, p.TKp, p.q_tr + tr, p.D4, s, at.lut);
+            dot_block<TAB, CW>(p.v_lane + lane_at, p.TKp, p.do_tr + tr, p.D4, dp, at.lut);
+            const uint32_t seen = at.part(seeing_rows(p, sp, k, rb * kAttnBlock));
+            const float* lse_at = p.rowlse + (int64_t)h * p.RQp + rb * kAttnBlock + at.off;
+            const float* delta_at = p.delta + (int64_t)h * p.RQp + rb * kAttnBlock + at.off;
+            each_value(s[0], [&](float v, int c) {
                 const float lse = lse_at[c];
                 float pr, ds;
                 score_gradient<false>(__builtin_fma((double)v, p.c, -((double)lse * 1.4426950408889634074)), lse, dp[0][0],
                                       delta_at[c], pr, ds);
                 const bool in = (seen >> c) & 1u;
 #pragma unroll
-                for (int i = 0; i < CPW - 1; ++i) dp[0][i] = dp[0][i + 1];
-                dp[0][CPW - 1] = in ? ds : 0.0f;
+                for (int i = 0; i < CW - 1; ++i) dp[0][i] = dp[0][i + 1];
+                dp[0][CW - 1] = in ? ds : 0.0f;
                 return in ? pr : 0.0f;
             });
         }
         const int nb = min(NW, k.b1 - rb0);
-        const int64_t first = row_at + (int64_t)rb0 * kAttnBlock * CPW;
+        const int64_t first = row_at + (int64_t)rb0 * kAttnBlock * 16;
         __syncthreads();                     // the last step's weights have been read
         if (mine) at.ex.template put<false>(at.w, s[0], p.M);
         __syncthreads();
-        if (live) weigh<TAB, false>(at.ex, nb, p.do_row + first, quad, dv, at.lut);
+        if (live) weigh<TAB, false>(at.ex, nb, p.do_row + first, dv, at.lut);
         __syncthreads();
         if (mine) at.ex.template put<true>(at.w, dp[0], p.M);
         __syncthreads();
-        if (live) weigh<TAB, true>(at.ex, nb, p.q_row + first, quad, dk, at.lut);
+        if (live) weigh<TAB, true>(at.ex, nb, p.q_row + first, dk, at.lut);
     }
     if (!live) return;
     store_key(p, k, h, split, at.w, dv, p.part0, p.dv, p.lddv, 1.0f);
@@ -873,12 +880,12 @@ __device__ __forceinline__ void dkv_tile_checked(const AttnParams& p, const Key&
 }
 
 // KEYS: dK and dV (tiles of keys), else dQ (tiles of rows).
-template <int TAB, bool KEYS>
-__global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_bwd_kernel(AttnParams p)
+template <int TAB, bool KEYS, int CW>
+__global__ __launch_bounds__((64 * max_waves<TAB, CW>()), (min_waves<TAB, CW>())) void attn_bwd_kernel(AttnParams p)
 {
     extern __shared__ __align__(16) unsigned char lds[];
     int* shared = reinterpret_cast<int*>(lds + table_lds<TAB>());
-    const Place<TAB> at(p, lds);
+    const Place<TAB, CW> at(p, lds);
     bool fast = !p.force_checked && p.elo == 1;
     int lo[4], hi[4];
 #pragma unroll
@@ -898,19 +905,19 @@ __global__ __launch_bounds__(max_threads<TAB>(), min_waves<TAB>()) void attn_bwd
         if constexpr (KEYS) {
             const Key k = tile_key(p, sp, split);
             if (!fast) {
-                if (live) dkv_tile_checked<TAB>(p, k, sp, h, split, at.w, at.lut);
+                if (live && at.w < p.NW) dkv_tile_checked<TAB>(p, k, sp, h, split, at.w, at.lut);
                 continue;
             }
             const int steps = most_steps(live ? (k.b1 - k.b0 + p.NW - 1) / p.NW : 0, at.tt, p.TT, shared);
-            dkv_tile<TAB>(p, at, k, sp, live, h, split, steps);
+            dkv_tile<TAB, CW>(p, at, k, sp, live, h, split, steps);
         } else {
             const Row r = tile_row(p, sp, split);
             if (!fast) {
-                if (live) dq_tile_checked<TAB>(p, r, sp, h, split, at.w, at.lut);
+                if (live && at.w < p.NW) dq_tile_checked<TAB>(p, r, sp, h, split, at.w, at.lut);
                 continue;
             }
             const int steps = most_steps(live ? (r.b1 - r.b0 + p.NW - 1) / p.NW : 0, at.tt, p.TT, shared);
-            dq_tile<TAB>(p, at, r, sp, live, h, split, steps);
+            dq_tile<TAB, CW>(p, at, r, sp, live, h, split, steps);
         }
     }
 }
@@ -960,35 +967,43 @@ hipError_t launch_join(const AttnJoinParams& p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles per workgroup: up to 8 waves; at M = 8, where one workgroup's table
-// fills a CU's LDS, as many as fit 12 waves and the LDS.
-template <int TAB>
+// Tiles per workgroup: as many as fit its waves and, at M = 8, the LDS.
+template <int TAB, int CW>
 static int tiles_per_group(int NW)
 {
-    if (TAB != AT_LDS8) return std::max(1, kMaxWaves / NW);
-    int n = std::max(1, 12 / NW);
-    while (n > 1 && table_lds<TAB>() + 64 + n * tile_bytes<TAB>(NW) > 163840) --n;
+    int n = std::max(1, max_waves<TAB, CW>() / (NW * (16 / CW)));
+    if (CW == 8) n = 1;                      // few tiles: a workgroup each
+    while (n > 1 && table_lds<TAB>() + 64 + n * tile_bytes<TAB>(NW, CW) > 163840) --n;
     return n;
 }
 
-template <int TAB, typename F>
+template <int TAB, int CW, typename F>
 static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s)
 {
-    p.TT = tiles_per_group<TAB>(p.NW);
+    p.TT = tiles_per_group<TAB, CW>(p.NW);
     p.items = (int64_t)((p.tiles + p.TT - 1) / p.TT) * p.K * p.splits;
-    const int threads = 64 * p.NW * p.TT;
-    const size_t lds = table_lds<TAB>() + 64 + (size_t)p.TT * tile_bytes<TAB>(p.NW);
+    const int threads = 64 * p.NW * (16 / CW) * p.TT;
+    const size_t lds = table_lds<TAB>() + 64 + (size_t)p.TT * tile_bytes<TAB>(p.NW, CW);
     const int slots = resident(cache, p.NW, reinterpret_cast<const void*>(f), threads, lds);
     if (slots < 1) return hipErrorInvalidValue;
     f<<<(unsigned)std::min<int64_t>(p.items, slots), threads, lds, s>>>(p);
     return hipGetLastError();
 }
 
+// Fewer waves of 16 columns than two per SIMD of the GPU's 256 CUs.
+// APPROX_ATTENTION_COLUMNS=8 or 16 forces a width (for measurements and tests).
+static bool few_waves(const AttnParams& p)
+{
+    const char* force = std::getenv("APPROX_ATTENTION_COLUMNS");
+    if (force != nullptr && (force[0] == '8' || force[0] == '1')) return force[0] == '8';
+    return (int64_t)p.tiles * p.K * p.splits * p.NW < 2048;
+}
+
 template <int TAB>
 static hipError_t run_fwd(const AttnParams& p, hipStream_t s)
 {
-    static Resident cache;
-    return run<TAB>(p, &attn_fwd_kernel<TAB>, cache, s);
+    static Resident narrow, wide;
+    return few_waves(p) ? run<TAB, 8>(p, &attn_fwd_kernel<TAB, 8>, narrow, s) : run<TAB, 16>(p, &attn_fwd_kernel<TAB, 16>, wide, s);
 }
 
 hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t s)
@@ -1008,8 +1023,10 @@ hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t s)
 template <int TAB>
 static hipError_t run_bwd(const AttnParams& p, bool keys, hipStream_t s)
 {
-    static Resident rows_cache, keys_cache;
-    return keys ? run<TAB>(p, &attn_bwd_kernel<TAB, true>, keys_cache, s) : run<TAB>(p, &attn_bwd_kernel<TAB, false>, rows_cache, s);
+    static Resident cache[4];
+    if (few_waves(p))
+        return keys ? run<TAB, 8>(p, &attn_bwd_kernel<TAB, true, 8>, cache[0], s) : run<TAB, 8>(p, &attn_bwd_kernel<TAB, false, 8>, cache[1], s);
+    return keys ? run<TAB, 16>(p, &attn_bwd_kernel<TAB, true, 16>, cache[2], s) : run<TAB, 16>(p, &attn_bwd_kernel<TAB, false, 16>, cache[3], s);
 }
 
 static hipError_t launch_sum(const AttnParams& p, bool keys, const float* part, float* out, int64_t ld, float scale, hipStream_t s)

@@ -261,30 +261,42 @@ __device__ __forceinline__ void fold_checked(uint32_t wa, uint32_t sa, const uin
     }
 }
 
-// acc[c] = FP32 sums, ascending over d, of T(row d, column c's d): the lane
-// panel's row at `lane` (Words at [D4 / 4][Rp][4]), 16 uniform columns at `tr`
-// ([D4][16]). Two steps at a time, their words requested two steps ahead.
-template <int TAB>
-__device__ __forceinline__ void dot_block(const Word* lane, int64_t Rp, const Word* tr, int D4, uint32_t quad,
-                                          float (&acc)[1][CPW], const Table& lut)
+// Uniform words of one step in NQ registers: 8 (NQ = 4) or 16 (NQ = 8) columns.
+template <int NQ>
+__device__ __forceinline__ void load_columns(const void* row, uint32_t (&q)[NQ])
 {
-    uint32_t wa[2][2], sa[2][2], q[2][2][UQ];
+    const uint4* src = reinterpret_cast<const uint4*>(row) + (threadIdx.x & 3u);
+    const uint4 a = src[0];
+    q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
+    if constexpr (NQ == 8) {
+        const uint4 b = src[4];
+        q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
+    }
+}
+
+// acc[c] = FP32 sums, ascending over d, of T(row d, column c's d): the lane
+// panel's row at `lane` (Words at [D4 / 4][Rp][4]), CW uniform columns at `tr`
+// (of [D4][16]). Two steps at a time, their words requested two steps ahead.
+template <int TAB, int CW>
+__device__ __forceinline__ void dot_block(const Word* lane, int64_t Rp, const Word* tr, int D4, float (&acc)[1][CW], const Table& lut)
+{
+    uint32_t wa[2][2], sa[2][2], q[2][2][CW / 2];
     auto load = [&](int s, int b) {
         const uint4 w = *reinterpret_cast<const uint4*>(lane + (int64_t)(s >> 1) * Rp * 4 + (s & 1) * 2);
         wa[b][0] = w.x + lut.lds; sa[b][0] = w.y; wa[b][1] = w.z + lut.lds; sa[b][1] = w.w;
-        load_uniform(tr + s * 32, quad, q[b][0]);
-        load_uniform(tr + s * 32 + 16, quad, q[b][1]);
+        load_columns(tr + s * 32, q[b][0]);
+        load_columns(tr + s * 32 + 16, q[b][1]);
     };
     const int steps = D4 / 2;                 // even
 #pragma unroll
-    for (int c = 0; c < CPW; ++c) acc[0][c] = 0.0f;
+    for (int c = 0; c < CW; ++c) acc[0][c] = 0.0f;
     load(0, 0);
 #pragma unroll 1
     for (int s = 0; s < steps; s += 2) {
         load(s + 1, 1);
-        fold<TAB, 2, 1>(wa[0], sa[0], q[0], acc, lut);
+        fold<TAB, 2, 1, CW, CW / 2>(wa[0], sa[0], q[0], acc, lut);
         load(min(s + 2, steps - 1), 0);
-        fold<TAB, 2, 1>(wa[1], sa[1], q[1], acc, lut);
+        fold<TAB, 2, 1, CW, CW / 2>(wa[1], sa[1], q[1], acc, lut);
     }
 }
 
@@ -341,21 +353,20 @@ __device__ __forceinline__ float exp2_once(double x)
     return x >= -64.0 ? v : 0.0f;
 }
 
-// f(element, its place) over a block's 16 values, in a loop of four (rotating
-// the registers) rather than unrolled: straight-line code runs at the speed
-// of its fetch the first time, which a short prompt's launch is made of.
-template <typename F>
-__device__ __forceinline__ void each_of_16(float (&x)[CPW], F f)
+// f(element, its place) over a block's CW values, in a loop of four (rotating
+// the registers): few temporaries at a time.
+template <int CW, typename F>
+__device__ __forceinline__ void each_value(float (&x)[CW], F f)
 {
 #pragma unroll 1
-    for (int g = 0; g < CPW; g += 4) {
+    for (int g = 0; g < CW; g += 4) {
         float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = f(x[i], g + i);
 #pragma unroll
-        for (int i = 0; i < CPW - 4; ++i) x[i] = x[i + 4];
+        for (int i = 0; i < CW - 4; ++i) x[i] = x[i + 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[CPW - 4 + i] = y[i];
+        for (int i = 0; i < 4; ++i) x[CW - 4 + i] = y[i];
     }
 }
 

@@ -92,19 +92,6 @@ struct PagedSpan {
     }
 };
 
-// Uniform words of one step: NR columns.
-template <int NQ>
-__device__ __forceinline__ void load_columns(const void* row, uint32_t (&q)[NQ])
-{
-    const uint4* src = reinterpret_cast<const uint4*>(row) + (threadIdx.x & 3u);
-    const uint4 a = src[0];
-    q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
-    if constexpr (NQ == 8) {
-        const uint4 b = src[4];
-        q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
-    }
-}
-
 // Four elements of a key, zero from D on.
 __device__ __forceinline__ uint4 key_four(const PagedParams& p, const float* row, int d)
 {

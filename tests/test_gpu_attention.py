@@ -107,8 +107,11 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("columns", ["8", "16"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}x{c[4]}x{c[5]}-{'causal' if c[6] else 'full'}")
-def test_forward_and_backward(am, case):
+def test_forward_and_backward(am, case, columns, monkeypatch):
+    """Both widths of a wave's share (the library takes 8 for small calls)."""
+    monkeypatch.setenv("APPROX_ATTENTION_COLUMNS", columns)
     name, ql, kl, H, K, D, causal = case
     mul = load(am, name)
     q, k, v, dout = inputs(9000 + 17 * D + H, ql, kl, H, K, D)
@@ -117,9 +120,11 @@ def test_forward_and_backward(am, case):
     backward_and_check(am, mul, q, k, v, dout, o, lse, cu_q, cu_k, causal, what=str(case))
 
 
-def test_long_reduction_in_chunks(am):
+@pytest.mark.parametrize("columns", ["8", "16"])
+def test_long_reduction_in_chunks(am, columns, monkeypatch):
     """Few rows over many keys (and many rows over few keys, backward): the
     ranges are split into chunks and joined."""
+    monkeypatch.setenv("APPROX_ATTENTION_COLUMNS", columns)
     mul = load(am, "mitchell07")
     for ql, kl in (([3], [1500]), ([700], [5])):
         q, k, v, dout = inputs(9100 + ql[0], ql, kl, 2, 1, 64)
