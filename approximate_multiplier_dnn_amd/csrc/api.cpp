@@ -13,6 +13,7 @@
 
 #include "../../include/approx_mul.h"
 #include "attention.h"
+#include "dense.h"
 #include "host.h"
 #include "internal.h"
 
@@ -445,12 +446,26 @@ int plan_finalize(Plan& pl, int M)
     return APPROX_OK;
 }
 
+// A dense layer's epilogue for a call whose reduction can end in it: `fused`
+// says whether it did.
+struct Finish {
+    const amx::EpilogueParams* e = nullptr;
+    bool fused = false;
+};
+
+hipError_t finish_reduce(const ReduceParams& rp, Finish* fin, hipStream_t stream)
+{
+    if (fin == nullptr) return amx::launch_reduce(rp, stream);
+    fin->fused = true;
+    return amx::launch_reduce_epilogue(rp, *fin->e, stream);
+}
+
 // Runs plans[0 .. count) as one call: one scratch request, one decode launch
 // for all their operands, the M = 8 copy choices, one GEMM-kernel launch and
 // each plan's reduction. count > 1 (at most kMaxGroup): plans of one grouped
 // kernel variant (amx::main_group_supported), each with its own stats block.
 int run_group(Plan* const* plans, int count, int dev, hipStream_t stream, const uint16_t* image, int M,
-              const ScratchSource& src)
+              const ScratchSource& src, Finish* fin = nullptr)
 {
     if (count < 1 || count > amx::kMaxGroup) return APPROX_EINVAL;
     size_t total = 0;
@@ -628,7 +643,7 @@ int run_group(Plan* const* plans, int count, int dev, hipStream_t stream, const 
         }
     }
     if (nred == 1 && red[0].variant != amx::RV_TILES) {
-        if (amx::launch_reduce(red[0].r, stream) != hipSuccess) return APPROX_EHIP;
+        if (finish_reduce(red[0].r, fin, stream) != hipSuccess) return APPROX_EHIP;
     } else if (nred == 1) {
         if (amx::launch_reduce_tiles(red[0].t, stream) != hipSuccess) return APPROX_EHIP;
     } else if (nred > 1) {
@@ -637,10 +652,10 @@ int run_group(Plan* const* plans, int count, int dev, hipStream_t stream, const 
     return APPROX_OK;
 }
 
-int run_plan(Plan& pl, int dev, hipStream_t stream, const uint16_t* image, int M, const ScratchSource& src)
+int run_plan(Plan& pl, int dev, hipStream_t stream, const uint16_t* image, int M, const ScratchSource& src, Finish* fin = nullptr)
 {
     Plan* plans[1] = {&pl};
-    return run_group(plans, 1, dev, stream, image, M, src);
+    return run_group(plans, 1, dev, stream, image, M, src, fin);
 }
 
 // Reduction split of the row-vector kernel (a function of the shapes and the
@@ -681,7 +696,8 @@ int64_t gemv_split(amx::GemvParams& g, int batch)
     return blocks * g.splits;
 }
 
-int gemv_run(amx::GemvParams& g, int batch, float* C, int dev, hipStream_t stream, const ScratchSource& src)
+int gemv_run(amx::GemvParams& g, int batch, float* C, int dev, hipStream_t stream, const ScratchSource& src,
+             Finish* fin = nullptr)
 {
     const int variant = gemv_variant_of(g.M, g.m, g.n);
     const int64_t items = gemv_split(g, batch);
@@ -737,7 +753,7 @@ int gemv_run(amx::GemvParams& g, int batch, float* C, int dev, hipStream_t strea
         rp.splits = g.splits;
         rp.batch = batch;
         rp.out_batch = g.out_batch;
-        if (amx::launch_reduce(rp, stream) != hipSuccess) return APPROX_EHIP;
+        if (finish_reduce(rp, fin, stream) != hipSuccess) return APPROX_EHIP;
     }
     return APPROX_OK;
 }
@@ -812,7 +828,7 @@ int gemm_check(int transA, int transB, int m, int n, int k, const float* A, int 
 int gemm_impl(int transA, int transB, int m, int n, int k, const float* A, int lda, long long strideA,
               const float* B, int ldb, long long strideB, float* C, int ldc, long long strideC, int batch,
               void* stream_v, const float* const* Ap = nullptr, const float* const* Bp = nullptr,
-              float* const* Cp = nullptr, bool noalloc = false)
+              float* const* Cp = nullptr, bool noalloc = false, Finish* fin = nullptr)
 {
     const bool arrays = Ap != nullptr || Bp != nullptr || Cp != nullptr;
     if (arrays && (Ap == nullptr || Bp == nullptr || Cp == nullptr)) return APPROX_EINVAL;
@@ -853,7 +869,7 @@ int gemm_impl(int transA, int transB, int m, int n, int k, const float* A, int l
         g.M = M; g.m = m; g.n = n; g.k = k; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.transA = transA;
         format_range(dev, &g.elo, &g.ehi);
         g.force_checked = force_checked() ? 1 : 0;
-        return gemv_run(g, batch, C, dev, stream, src);
+        return gemv_run(g, batch, C, dev, stream, src, fin);
     }
 
     Plan pl;
@@ -870,7 +886,7 @@ int gemm_impl(int transA, int transB, int m, int n, int k, const float* A, int l
     pl.mp.ldc = ldc;
     pl.lane.ld = lda;
     pl.uni.ld = ldb;
-    return run_plan(pl, dev, stream, image, M, src);
+    return run_plan(pl, dev, stream, image, M, src, fin);
 }
 
 struct ConvShape {
@@ -1301,6 +1317,15 @@ int amx::host_table(amx::HostTable* t)
     format_range(t->dev, &t->elo, &t->ehi);
     t->force_checked = force_checked() ? 1 : 0;
     return APPROX_OK;
+}
+
+int amx::host_dense(int m, int n, int k, const float* X, int ldx, const float* W, int ldw, float* sums, int lds,
+                    const EpilogueParams& e, bool* fused, hipStream_t stream)
+{
+    Finish fin{&e, false};
+    const int rc = gemm_impl(0, 0, m, n, k, X, ldx, 0, W, ldw, 0, sums, lds, 0, 1, stream, nullptr, nullptr, nullptr, false, &fin);
+    *fused = fin.fused;
+    return rc;
 }
 
 int amx::host_kept(int dev, hipStream_t stream, size_t bytes, char** out)

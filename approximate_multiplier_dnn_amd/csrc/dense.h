@@ -19,6 +19,10 @@ struct EpilogueParams {
     int vec;                  // n and every leading dimension multiples of 4, every pointer 16-byte aligned
 };
 hipError_t launch_epilogue(const EpilogueParams& p, hipStream_t s);
+// The reduction of a GEMM's chunk partials (launch_reduce; batch 1) that ends
+// in the epilogue (`sums` is not read).
+struct ReduceParams;
+hipError_t launch_reduce_epilogue(const ReduceParams& p, const EpilogueParams& e, hipStream_t s);
 
 struct DzParams {
     const float* dy;

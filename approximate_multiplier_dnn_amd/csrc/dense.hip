@@ -3,21 +3,9 @@
 // the bias gradient. The products run in kernels.hip.
 #include <algorithm>
 
-#include "dense.h"
+#include "dense_device.h"
 
 namespace amx {
-
-// Activations on FP32 (forward): Phi(z) = erfc(-z / sqrt 2) / 2 keeps its
-// relative accuracy for negative z, where 1 + erf cancels.
-__device__ __forceinline__ float activate(float z, int act)
-{
-    switch (act) {
-    case ACT_RELU: return z < 0.0f ? 0.0f : z;                  // NaN stays
-    case ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    case ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
-    }
-}
 
 // Derivatives in 64 bits: dz enters the multiplier's table, which cuts it at M
 // bits, so it is rounded once (an error of one last place next to such a
@@ -58,12 +46,7 @@ __global__ __launch_bounds__(256) void epilogue_kernel(EpilogueParams p)
             }
             reinterpret_cast<float4*>(p.y + i * p.ldy)[j] = z;
         } else {
-            float z = p.sums[i * p.lds + j];
-            if (p.bias != nullptr) z += p.bias[j];
-            if (p.z != nullptr) p.z[i * p.ldz + j] = z;
-            z = activate(z, p.act);
-            if (p.residual != nullptr) z += p.residual[i * p.ldr + j];
-            p.y[i * p.ldy + j] = z;
+            finish_output(p, i, j, p.sums[i * p.lds + j]);
         }
     }
 }

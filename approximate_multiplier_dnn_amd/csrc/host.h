@@ -26,4 +26,11 @@ int host_scratch(int dev, hipStream_t stream, size_t bytes, char** out);
 // The stream's second scratch block, which GEMM calls leave alone.
 int host_kept(int dev, hipStream_t stream, size_t bytes, char** out);
 
+struct EpilogueParams;
+
+// sums = X W as approx_gemm; *fused: the reduction ended in the epilogue
+// (which is then done, and sums is not written).
+int host_dense(int m, int n, int k, const float* X, int ldx, const float* W, int ldw, float* sums, int lds,
+               const EpilogueParams& e, bool* fused, hipStream_t stream);
+
 }  // namespace amx

