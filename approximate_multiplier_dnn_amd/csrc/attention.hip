@@ -29,8 +29,9 @@ namespace amx {
 
 // Decodes 64 rows of one kv head per step through LDS into the panels asked
 // for. Bound by HBM: 4 bytes read and 8 written per element and panel.
-// (8192 tokens of 3 x 12 heads of 64, 226 MB: 22 us; with 256 workgroups
-// per tensor and LDS for 128 columns, too few in flight: 66 us.)
+// (8192 tokens of 3 x 12 heads of 64, 226 MB: 50 us, 4.5 TB/s, where a large
+// copy moves 4.9; with 256 workgroups per tensor and LDS for 128 columns, too
+// few in flight: 66 us.)
 constexpr int kDecodeThreads = 256;
 __global__ __launch_bounds__(kDecodeThreads) void attn_decode_kernel(AttnDecodeParams p)
 {
@@ -880,9 +881,14 @@ __device__ __forceinline__ void dkv_tile_checked(const AttnParams& p, const Key&
     }
 }
 
-// KEYS: dK and dV (tiles of keys), else dQ (tiles of rows).
+// KEYS: dK and dV (tiles of keys), else dQ (tiles of rows). Three waves per
+// SIMD and up to 4 waves per workgroup (8 for D above 64) rather than the
+// forward pass's four and 8: with 128 registers these spill (8 ragged
+// sequences up to 512, 12/4 heads of 64: dQ 365 -> 318 us, dK and dV 452 ->
+// 377; 8 heads of 128: 780 -> 529 and 920 -> 692). The forward pass loses by
+// the same change (8 heads of 128: 661 -> 850 us).
 template <int TAB, bool KEYS, int CW>
-__global__ __launch_bounds__((64 * max_waves<TAB, CW>()), (min_waves<TAB, CW>())) void attn_bwd_kernel(AttnParams p)
+__global__ __launch_bounds__((64 * max_waves<TAB, CW>()), (CW == 16 ? 3 : 4)) void attn_bwd_kernel(AttnParams p)
 {
     extern __shared__ __align__(16) unsigned char lds[];
     int* shared = reinterpret_cast<int*>(lds + table_lds<TAB>());
@@ -968,20 +974,20 @@ hipError_t launch_join(const AttnJoinParams& p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles per workgroup: as many as fit its waves and, at M = 8, the LDS.
+// Tiles per workgroup: as many as fit its waves (`most` at run) and, at M = 8, the LDS.
 template <int TAB, int CW>
 static int tiles_per_group(int NW)
 {
     int n = std::max(1, max_waves<TAB, CW>() / (NW * (16 / CW)));
     if (CW == 8) n = 1;                      // few tiles: a workgroup each
-    while (n > 1 && table_lds<TAB>() + 64 + n * tile_bytes<TAB>(NW, CW) > 163840) --n;
+    while (n > 1 && table_lds<TAB>() + 64 + n * tile_bytes<TAB>(NW, CW) > kLdsBytes) --n;
     return n;
 }
 
 template <int TAB, int CW, typename F>
-static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s)
+static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s, int most = 16)
 {
-    p.TT = tiles_per_group<TAB, CW>(p.NW);
+    p.TT = std::max(1, std::min(tiles_per_group<TAB, CW>(p.NW), most / p.NW));
     p.items = (int64_t)((p.tiles + p.TT - 1) / p.TT) * p.K * p.splits;
     const int threads = 64 * p.NW * (16 / CW) * p.TT;
     const size_t lds = table_lds<TAB>() + 64 + (size_t)p.TT * tile_bytes<TAB>(p.NW, CW);
@@ -1027,7 +1033,7 @@ static hipError_t run_bwd(const AttnParams& p, bool keys, hipStream_t s)
     static Resident cache[4];
     if (few_waves(p))
         return keys ? run<TAB, 8>(p, &attn_bwd_kernel<TAB, true, 8>, cache[0], s) : run<TAB, 8>(p, &attn_bwd_kernel<TAB, false, 8>, cache[1], s);
-    return keys ? run<TAB, 16>(p, &attn_bwd_kernel<TAB, true, 16>, cache[2], s) : run<TAB, 16>(p, &attn_bwd_kernel<TAB, false, 16>, cache[3], s);
+    return keys ? run<TAB, 16>(p, &attn_bwd_kernel<TAB, true, 16>, cache[2], s, TAB == AT_LDS8 ? 16 : 4) : run<TAB, 16>(p, &attn_bwd_kernel<TAB, false, 16>, cache[3], s, TAB == AT_LDS8 ? 16 : 4);
 }
 
 static hipError_t launch_sum(const AttnParams& p, bool keys, const float* part, float* out, int64_t ld, float scale, hipStream_t s)

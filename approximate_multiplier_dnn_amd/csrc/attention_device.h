@@ -394,8 +394,9 @@ constexpr int table_lds()
 }
 
 // Resident workgroups of a kernel on the current device (queried once per
-// device, kernel and configuration `slot`), after allowing it `lds` bytes of
-// dynamic LDS.
+// device, kernel and configuration `slot`), after allowing it all of a CU's
+// LDS as dynamic LDS.
+constexpr int kLdsBytes = 163840;
 constexpr int kMaxGpus = 64;
 constexpr int kMaxConfigs = 16;
 struct Resident {
@@ -408,7 +409,7 @@ inline int resident(Resident& cache, int slot, const void* f, int threads, size_
     int n = cache.n[dev][slot].load(std::memory_order_relaxed);
     if (n == 0) {
         int cus = 0, per = 0;
-        if (lds > 0 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess) return 0;
+        if (lds > 0 && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes) != hipSuccess) return 0;
         if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) return 0;
         if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, f, threads, lds) != hipSuccess || per < 1) return 0;
         n = cus * per;

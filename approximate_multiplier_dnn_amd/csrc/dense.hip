@@ -92,7 +92,7 @@ hipError_t launch_epilogue(const EpilogueParams& p, hipStream_t s)
 
 hipError_t launch_dz(const DzParams& p, float* db, hipStream_t s)
 {
-    const int chunks = (p.m + p.rows - 1) / p.rows;
+    const int chunks = std::max(1, (p.m + p.rows - 1) / p.rows);      // no row: db = 0
     dz_kernel<<<dim3((p.n + 63) / 64, chunks), 256, 0, s>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || db == nullptr) return e;

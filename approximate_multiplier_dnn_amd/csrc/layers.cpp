@@ -21,6 +21,8 @@ using amx::Word;
 
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+// Scales whose 64-bit scores and FP32 gradients stay in range.
+constexpr double kLeastScale = 0x1p-100, kMostScale = 0x1p100;
 // Rows per sequence (tokens x heads of a group) from which a paged call
 // decodes the cache into panels for the packed kernel, and the panels' limit.
 // Four chunks of 128 tokens (256 rows) over up to 4000 keys: 510 us in blocks
@@ -49,7 +51,7 @@ struct Carver {
 int check_heads(int nseq, int heads, int kv_heads, int dim, int total_q, double scale)
 {
     if (nseq < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || dim < 1 || total_q < 0) return APPROX_EINVAL;
-    if (!std::isfinite(scale) || !(scale > 0.0)) return APPROX_EINVAL;
+    if (!(scale >= kLeastScale && scale <= kMostScale)) return APPROX_EINVAL;      // NaN too
     if (dim > amx::kAttnMaxDim) return APPROX_EUNSUPPORTED;
     if ((int64_t)total_q * heads >= kMaxRows) return APPROX_EUNSUPPORTED;
     return APPROX_OK;

@@ -354,8 +354,8 @@ int approx_conv2d_chunks(int pass, int N, int H, int W, int C, int K, int R, int
  * wrong ones give wrong rows but no access outside the tensors. total_q and
  * total_k are the tokens of the tensors.
  * Errors: APPROX_EINVAL (sizes, heads not a multiple of kv_heads, a leading
- * dimension below heads * dim, causal not 0 or 1, scale not finite and
- * positive, NULL pointers), APPROX_EUNSUPPORTED (dim above 128, 2^30 rows or
+ * dimension below heads * dim, causal not 0 or 1, scale outside [2^-100,
+ * 2^100], NULL pointers), APPROX_EUNSUPPORTED (dim above 128, 2^30 rows or
  * more), APPROX_ENOLUT, APPROX_EHIP.
  */
 int approx_attention_fwd(int nseq, int heads, int kv_heads, int dim, int total_q, int total_k,

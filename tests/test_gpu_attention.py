@@ -133,6 +133,18 @@ def test_long_reduction_in_chunks(am, columns, monkeypatch):
         backward_and_check(am, mul, q, k, v, dout, o, lse, cu_q, cu_k, False, what="long")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_sequences_than_a_wave(am, causal):
+    """Seventy-odd sequences, empty ones among them."""
+    mul = load(am, "mitchell07")
+    lens = [int(n) for n in np.random.RandomState(7).randint(0, 9, 75)]
+    lens[3], lens[70] = 0, 70
+    q, k, v, dout = inputs(9150, lens, lens, 2, 1, 32)
+    cu = ref.packed(lens)
+    o, lse = forward_and_check(am, mul, q, k, v, cu, cu, causal, what="many")
+    backward_and_check(am, mul, q, k, v, dout, o, lse, cu, cu, causal, what="many")
+
+
 def test_rising_scores_move_the_maximum(am):
     """Scores that rise by tens of powers of two along the keys: every block
     raises the running maximum, and the early weights vanish (below 2^-64)."""

@@ -171,6 +171,16 @@ def test_views_subsets_and_graph(am):
     assert torch.equal(only, eager[2])
 
 
+def test_no_rows(am):
+    """A batch without rows: nothing forward, zero gradients of w and the bias."""
+    load(am, "mitchell07")
+    x, w, e = torch.zeros(0, 5, device="cuda"), dev(normal(7290, (5, 6))), torch.zeros(0, 6, device="cuda")
+    assert am.dense_fwd(x, w, act="gelu").shape == (0, 6)
+    dx, dw, db = am.dense_bwd(e, x, w, z=e, act="gelu", bias=True)
+    torch.cuda.synchronize()
+    assert dx.shape == (0, 5) and (dw == 0).all() and (db == 0).all()
+
+
 def test_gradient_against_differences(am):
     """Native multiplier: a layer's gradients along random directions against
     central differences of the 64-bit layer."""

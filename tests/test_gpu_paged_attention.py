@@ -103,6 +103,14 @@ def test_against_definition(am, case):
         check(am, mul, q, kp, vp, table, new, k_len, causal=False, what=str(case))
 
 
+def test_more_sequences_than_a_wave(am):
+    mul = load(am, "mitchell07")
+    k_len = [int(n) for n in np.random.RandomState(8).randint(0, 40, 70)]
+    new = [min(1, n) for n in k_len]
+    kp, vp, table = cache(8050, k_len, 16, 1, 32)
+    check(am, mul, normal(8051, (sum(new), 2, 32)), kp, vp, table, new, k_len, what="many")
+
+
 def test_same_result_as_packed(am):
     """The whole prompt as one chunk over the cache is the packed call."""
     mul = load(am, "mitchell07")

@@ -26,7 +26,7 @@ BWD = ["nseq", "heads", "kv_heads", "dim", "total_q", "total_k", "cu_q", "cu_k",
 PAGED = dict(nseq=2, heads=4, kv_heads=2, dim=64, total_q=3, cu_q=P, num_pages=5, page=16, kp=P, vp=P, table=P, table_ld=4, k_len=P,
              causal=1, scale=0.125, q=P, ldq=256, o=P, ldo=256, lse=None, stream=None)
 WRONG = [dict(nseq=-1), dict(heads=0), dict(heads=3), dict(kv_heads=0), dict(dim=0), dict(total_q=-1), dict(causal=2),
-         dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(ldq=255), dict(ldo=255), dict(q=None),
+         dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=1e300), dict(scale=1e-300), dict(ldq=255), dict(ldo=255), dict(q=None),
          dict(o=None), dict(cu_q=None)]
 
 
