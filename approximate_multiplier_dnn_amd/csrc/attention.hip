@@ -13,12 +13,13 @@
 // scales the sums by a power of two and changes no mantissa, so one pass over
 // the keys gives the two-pass result, and chunks of keys join exactly.
 //
-// One wave owns 64 rows, one per lane, and takes 16 keys at a time. The keys
-// (and then the values' columns) are uniform operands spread over the lanes
-// of each quad (product.h); the scores of a block come out in the lanes that
-// need them as the lane operand of P V, so they never leave the registers.
-// What bounds the loops is the rate of table lookups (one 16-bit LDS read per
-// product), as in the GEMM kernel.
+// A tile is 64 rows of a kv head, one per lane, and its waves share each step
+// of 16 (or, in calls that leave the GPU mostly empty, 8) keys per wave: wave
+// w computes the scores of its own keys, hands their numerators to the others
+// through LDS, and sums its own 16 (or 8) value columns over all the step's
+// keys. The keys, then the values' columns, are uniform operands spread over
+// the lanes of each quad (product.h). What bounds the loops is the rate of
+// table lookups (one 16-bit LDS read per product), as in the GEMM kernel.
 #include "attention_device.h"
 
 #include <cstdlib>

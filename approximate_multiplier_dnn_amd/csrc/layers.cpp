@@ -1,6 +1,6 @@
 // layers.cpp -- the C ABI's attention and dense-layer calls: argument checks,
 // panel layouts in the stream's scratch arena, and launch plans. Every
-// arithmetic step runs in attention.hip and kernels.hip.
+// arithmetic step runs in attention.hip, paged.hip, dense.hip and kernels.hip.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -64,11 +64,12 @@ bool too_small(int ld, int heads, int dim) { return ld < (int64_t)heads * dim; }
 int score_limit(double c) { return 254 + 40 - 9 - (int)std::ceil(std::log2(c)); }
 
 // Chunks of each tile's range, so that the items (tiles x chunks) are about
-// three for each of 768 resident workgroups, and a chunk keeps at least two
-// steps of 16 NW of the average range. A function of the shapes only.
+// 2304 (three or more for each workgroup's turn at the counter), and a chunk
+// keeps at least two steps of 16 NW of the average range. A function of the
+// shapes only.
 int split_for(int64_t tiles, int64_t blocks, int NW)
 {
-    constexpr int64_t kItems = 3 * 768;
+    constexpr int64_t kItems = 2304;
     const int64_t want = cdiv(kItems, std::max<int64_t>(1, tiles));
     return (int)std::max<int64_t>(1, std::min<int64_t>({want, blocks / (2 * NW), amx::kAttnMaxSplits}));
 }
