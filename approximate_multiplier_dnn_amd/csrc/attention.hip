@@ -882,12 +882,13 @@ __device__ __forceinline__ void dkv_tile_checked(const AttnParams& p, const Key&
     }
 }
 
-// KEYS: dK and dV (tiles of keys), else dQ (tiles of rows). Three waves per
-// SIMD and up to 4 waves per workgroup (8 for D above 64) rather than the
-// forward pass's four and 8: with 128 registers these spill (8 ragged
-// sequences up to 512, 12/4 heads of 64: dQ 365 -> 318 us, dK and dV 452 ->
-// 377; 8 heads of 128: 780 -> 529 and 920 -> 692). The forward pass loses by
-// the same change (8 heads of 128: 661 -> 850 us).
+// KEYS: dK and dV (tiles of keys), else dQ (tiles of rows). Waves of 8 columns
+// (run_bwd), whose sums fit the 128 registers of four waves per SIMD; with 16
+// columns these spill, and three waves per SIMD are left (8 ragged sequences
+// up to 512, 12/4 heads of 64: dQ 301 us, dK and dV 373; with 8 columns 254
+// and 338). The forward pass has half the sums and loses by either change (16
+// x 512 tokens, 12 heads of 64: 529 -> 560 us with 8 columns; 8 heads of 128,
+// 661 -> 850 us with three waves).
 template <int TAB, bool KEYS, int CW>
 __global__ __launch_bounds__((64 * max_waves<TAB, CW>()), (CW == 16 ? 3 : 4)) void attn_bwd_kernel(AttnParams p)
 {
@@ -975,20 +976,20 @@ hipError_t launch_join(const AttnJoinParams& p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles per workgroup: as many as fit its waves (`most` at run) and, at M = 8, the LDS.
+// Tiles per workgroup: as many as fit its waves and, at M = 8, the LDS.
 template <int TAB, int CW>
 static int tiles_per_group(int NW)
 {
     int n = std::max(1, max_waves<TAB, CW>() / (NW * (16 / CW)));
-    if (CW == 8) n = 1;                      // few tiles: a workgroup each
+    if (CW == 8) n = 1;                      // few tiles, or many sums: a workgroup each
     while (n > 1 && table_lds<TAB>() + 64 + n * tile_bytes<TAB>(NW, CW) > kLdsBytes) --n;
     return n;
 }
 
 template <int TAB, int CW, typename F>
-static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s, int most = 16)
+static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s)
 {
-    p.TT = std::max(1, std::min(tiles_per_group<TAB, CW>(p.NW), most / p.NW));
+    p.TT = tiles_per_group<TAB, CW>(p.NW);
     p.items = (int64_t)((p.tiles + p.TT - 1) / p.TT) * p.K * p.splits;
     const int threads = 64 * p.NW * (16 / CW) * p.TT;
     const size_t lds = table_lds<TAB>() + 64 + (size_t)p.TT * tile_bytes<TAB>(p.NW, CW);
@@ -998,8 +999,10 @@ static hipError_t run(AttnParams p, F* f, Resident& cache, hipStream_t s, int mo
     return hipGetLastError();
 }
 
-// Fewer waves of 16 columns than two per SIMD of the GPU's 256 CUs.
-// APPROX_ATTENTION_COLUMNS=8 or 16 forces a width (for measurements and tests).
+// Fewer waves of 16 columns than two per SIMD of the GPU's 256 CUs (five
+// prompts of up to 48 tokens: 51 us with 16 columns, 36 with 8; 16 x 512
+// tokens, 12 heads of 64: 529 and 560).
+// APPROX_ATTENTION_COLUMNS=8 or 16 forces a side (for measurements and tests).
 static bool few_waves(const AttnParams& p)
 {
     const char* force = std::getenv("APPROX_ATTENTION_COLUMNS");
@@ -1028,13 +1031,22 @@ hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t s)
                                       p.part_l, p.o, p.ldo, p.lse}, s);
 }
 
+// 8 columns per wave: 2 to 24% faster than 16 at M = 4 and 7 (D = 32 to 128,
+// calls that fill the GPU and calls that do not), 1 to 11% at M = 10 (2% slower
+// at D = 128). At M = 8 one workgroup's table fills a CU, so that a tile of 8
+// columns with D up to 32 leaves it at 2 or 4 waves: 8 sequences up to 512, 12/4
+// heads of 32: 770 us with 8 columns, 555 with 16 and more tiles.
 template <int TAB>
 static hipError_t run_bwd(const AttnParams& p, bool keys, hipStream_t s)
 {
     static Resident cache[4];
-    if (few_waves(p))
-        return keys ? run<TAB, 8>(p, &attn_bwd_kernel<TAB, true, 8>, cache[0], s) : run<TAB, 8>(p, &attn_bwd_kernel<TAB, false, 8>, cache[1], s);
-    return keys ? run<TAB, 16>(p, &attn_bwd_kernel<TAB, true, 16>, cache[2], s, TAB == AT_LDS8 ? 16 : 4) : run<TAB, 16>(p, &attn_bwd_kernel<TAB, false, 16>, cache[3], s, TAB == AT_LDS8 ? 16 : 4);
+    if constexpr (TAB == AT_LDS8) {
+        if (p.NW <= 2 && !few_waves(p))
+            return keys ? run<TAB, 16>(p, &attn_bwd_kernel<TAB, true, 16>, cache[2], s)
+                        : run<TAB, 16>(p, &attn_bwd_kernel<TAB, false, 16>, cache[3], s);
+    }
+    return keys ? run<TAB, 8>(p, &attn_bwd_kernel<TAB, true, 8>, cache[0], s)
+                : run<TAB, 8>(p, &attn_bwd_kernel<TAB, false, 8>, cache[1], s);
 }
 
 static hipError_t launch_sum(const AttnParams& p, bool keys, const float* part, float* out, int64_t ld, float scale, hipStream_t s)

@@ -133,6 +133,19 @@ def test_long_reduction_in_chunks(am, columns, monkeypatch):
         backward_and_check(am, mul, q, k, v, dout, o, lse, cu_q, cu_k, False, what="long")
 
 
+@pytest.mark.parametrize("columns", ["8", "16"])
+@pytest.mark.parametrize("dim", [24, 32])
+def test_small_heads_with_a_wide_table(am, dim, columns, monkeypatch):
+    """M = 8 and heads of up to 32: the backward pass takes either width."""
+    monkeypatch.setenv("APPROX_ATTENTION_COLUMNS", columns)
+    mul = load(am, "perturbed08")
+    ql, kl = [70, 1, 33], [70, 20, 33]
+    q, k, v, dout = inputs(9300 + dim, ql, kl, 4, 2, dim)
+    cu_q, cu_k = ref.packed(ql), ref.packed(kl)
+    o, lse = forward_and_check(am, mul, q, k, v, cu_q, cu_k, True, what="small heads")
+    backward_and_check(am, mul, q, k, v, dout, o, lse, cu_q, cu_k, True, what="small heads")
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_more_sequences_than_a_wave(am, causal):
     """Seventy-odd sequences, empty ones among them."""
